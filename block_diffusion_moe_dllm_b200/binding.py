@@ -56,6 +56,26 @@ class UnmaskDesc(C.Structure):
                 ("dtype", i32), ("score", i32), ("cfg_image_scale", f32)]
 
 
+class Kv8StoreDesc(C.Structure):
+    _fields_ = [("B", i32), ("Hkv", i32), ("d", i32), ("n", i32), ("cap_src", i32), ("src_row", i32), ("cap", i32),
+                ("dst_row", i32), ("scale_len", i32), ("dtype", i32), ("pos_stride", i32)]
+
+
+class AttnKv8Desc(C.Structure):
+    _fields_ = [("B", i32), ("Lq", i32), ("Hq", i32), ("Hkv", i32), ("d", i32), ("blk_len", i32), ("P", i32),
+                ("cap", i32), ("cap_own", i32), ("scale_len", i32), ("dtype", i32), ("scale", f32)]
+
+
+class AttnMassDesc(C.Structure):
+    _fields_ = [("B", i32), ("Lq", i32), ("Hq", i32), ("Hkv", i32), ("d", i32), ("P", i32), ("cap", i32),
+                ("scale_len", i32), ("dtype", i32), ("scale", f32), ("decay", f32)]
+
+
+class Kv8EvictDesc(C.Structure):
+    _fields_ = [("B", i32), ("Hkv", i32), ("d", i32), ("P", i32), ("cap", i32), ("n_keep", i32), ("cap_out", i32),
+                ("scale_len", i32), ("n_first", i32), ("n_last", i32), ("per_head", i32)]
+
+
 class Layer(C.Structure):
     _fields_ = [("attn_norm", vp), ("w_qkv", vp), ("w_o", vp), ("ffn_norm", vp), ("w_router", vp),
                 ("router_bias", vp), ("w_gu", vp), ("w_down", vp), ("w_gu_shared", vp), ("w_down_shared", vp),
@@ -108,6 +128,13 @@ _SIGS = {
     "dllm_unmask": ([C.POINTER(UnmaskDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
     "dllm_unmask_workspace_size": ([C.POINTER(UnmaskDesc)], sz),
     "dllm_unmask_noalloc": ([C.POINTER(UnmaskDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], C.c_int),
+    "dllm_kv8_store": ([C.POINTER(Kv8StoreDesc)] + [vp] * 9, C.c_int),
+    "dllm_block_attn_kv8": ([C.POINTER(AttnKv8Desc)] + [vp] * 11 + [sz, vp], C.c_int),
+    "dllm_block_attn_kv8_workspace_size": ([C.POINTER(AttnKv8Desc)], sz),
+    "dllm_attn_mass_kv8": ([C.POINTER(AttnMassDesc)] + [vp] * 8 + [sz, vp], C.c_int),
+    "dllm_attn_mass_kv8_workspace_size": ([C.POINTER(AttnMassDesc)], sz),
+    "dllm_kv8_evict": ([C.POINTER(Kv8EvictDesc)] + [vp] * 15 + [sz, vp], C.c_int),
+    "dllm_kv8_evict_workspace_size": ([C.POINTER(Kv8EvictDesc)], sz),
     "dllm_denoise_step": ([C.POINTER(Model), C.POINTER(State), C.POINTER(StepParams), vp, sz, vp], C.c_int),
     "dllm_denoise_step_workspace_size": ([C.POINTER(Model), C.POINTER(State), C.POINTER(StepParams)], sz),
     "dllm_denoise_step_views": ([C.POINTER(Model), C.POINTER(State), C.POINTER(StepParams), vp, sz,
@@ -260,6 +287,63 @@ def unmask(logits, row_pos, n_rows_dev, tokens, mask, sel, nsel, conf, remaining
     return check(lib.dllm_unmask(C.byref(desc), ptr(logits), ptr(row_pos), ptr(n_rows_dev), ptr(tokens), ptr(mask),
                                  ptr(sel), ptr(nsel), ptr(conf), ptr(remaining), ws.addr, ws.nbytes,
                                  stream_handle(stream)))
+
+
+def _device_stream(t, stream):
+    """The stream's handle, after checking that the call's tensors are on the current device (the library launches
+    there)."""
+    import torch
+    if t.get_device() != torch.cuda.current_device():
+        raise DllmError(ERR_INVALID_ARG, f"tensors on device {t.get_device()}, current device "
+                                         f"{torch.cuda.current_device()}")
+    return stream_handle(stream)
+
+
+def kv8_store(k, v, k_codes, v_codes, k_scale, v_scale, B, Hkv, d, n, cap_src, cap, scale_len, dtype, src_row=0,
+              dst_row=0, src_pos=None, dst_rows=None, pos_stride=None, stream=None):
+    """Quantise n rows of K and V of every (row, kv head) into the 8-bit cache (E4M3 codes, a scale per run)."""
+    lib = load()
+    desc = Kv8StoreDesc(B, Hkv, d, n, cap_src, src_row, cap, dst_row, scale_len, dtype,
+                        n if pos_stride is None else pos_stride)
+    return check(lib.dllm_kv8_store(C.byref(desc), ptr(k), ptr(v), ptr(src_pos), ptr(dst_rows), ptr(k_codes),
+                                    ptr(v_codes), ptr(k_scale), ptr(v_scale), _device_stream(k_codes, stream)))
+
+
+def block_attn_kv8(q, k_codes, v_codes, k_scale, v_scale, out, B, Lq, Hq, Hkv, d, P, cap, scale_len, blk_len, dtype,
+                   prefix_len=None, k_own=None, v_own=None, cap_own=0, lse=None, scale=0.0, ws=None, stream=None):
+    """Attention over an 8-bit prefix of each row's own length and the queries' own K/V in the storage type."""
+    lib = load()
+    desc = AttnKv8Desc(B, Lq, Hq, Hkv, d, blk_len, P, cap, cap_own, scale_len, dtype, scale)
+    need = lib.dllm_block_attn_kv8_workspace_size(C.byref(desc))
+    ws = (ws or Workspace(need, q.device)).ensure(need)
+    return check(lib.dllm_block_attn_kv8(C.byref(desc), ptr(q), ptr(k_codes), ptr(v_codes), ptr(k_scale),
+                                         ptr(v_scale), ptr(prefix_len), ptr(k_own), ptr(v_own), ptr(out), ptr(lse),
+                                         ws.addr, ws.nbytes, _device_stream(q, stream)))
+
+
+def attn_mass_kv8(q, k_codes, k_scale, lse, mass_in, mass_out, B, Lq, Hq, Hkv, d, P, cap, scale_len, dtype,
+                  prefix_len=None, scale=0.0, decay=1.0, ws=None, stream=None):
+    """mass_out = decay * mass_in + the attention weight of the queries on every prefix row, per kv head."""
+    lib = load()
+    desc = AttnMassDesc(B, Lq, Hq, Hkv, d, P, cap, scale_len, dtype, scale, decay)
+    need = lib.dllm_attn_mass_kv8_workspace_size(C.byref(desc))
+    ws = (ws or Workspace(need, q.device)).ensure(need)
+    return check(lib.dllm_attn_mass_kv8(C.byref(desc), ptr(q), ptr(k_codes), ptr(k_scale), ptr(prefix_len), ptr(lse),
+                                        ptr(mass_in), ptr(mass_out), ws.addr, ws.nbytes, _device_stream(q, stream)))
+
+
+def kv8_evict(k_codes, v_codes, k_scale, v_scale, mass, k_out, v_out, k_scale_out, v_scale_out, mass_out, keep_pos,
+              len_out, B, Hkv, d, P, cap, n_keep, cap_out, scale_len, n_first=0, n_last=0, per_head=0,
+              prefix_len=None, pos=None, ws=None, stream=None):
+    """The cache reduced to the first, the last and the most attended rows, compacted into another 8-bit cache."""
+    lib = load()
+    desc = Kv8EvictDesc(B, Hkv, d, P, cap, n_keep, cap_out, scale_len, n_first, n_last, per_head)
+    need = lib.dllm_kv8_evict_workspace_size(C.byref(desc))
+    ws = (ws or Workspace(need, mass.device)).ensure(need)
+    return check(lib.dllm_kv8_evict(C.byref(desc), ptr(k_codes), ptr(v_codes), ptr(k_scale), ptr(v_scale), ptr(mass),
+                                    ptr(prefix_len), ptr(pos), ptr(k_out), ptr(v_out), ptr(k_scale_out),
+                                    ptr(v_scale_out), ptr(mass_out), ptr(keep_pos), ptr(len_out), ws.addr, ws.nbytes,
+                                    _device_stream(mass, stream)))
 
 
 def status_check(ws, stream=None):

@@ -7,6 +7,7 @@
 #include <cmath>
 #include "common.cuh"
 #include "kernels.h"
+#include "kv8.h"
 #include "misc.h"
 #include "tc.cuh"
 
@@ -511,6 +512,187 @@ int dllm_prefix_retain(const dllm_retain_desc* d, const void* k_cache, const voi
   a.conf = conf; a.conf_stride = d->P; a.alpha = conf ? d->alpha : 1.f; a.modality = modality;
   a.n_keep_img = d->n_keep_img;
   return launch_retain(a, stream);
+}
+
+// ------------------------------------------------------------------------------------------------ 8-bit KV cache
+namespace {
+
+// Arrays of na and nb bytes share memory.
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x < y + nb && y < x + na;
+}
+
+int check_kv8_format(const char* who, int d, int scale_len) {
+  REQ(d >= 16 && d <= 128 && d % 16 == 0, DLLM_ERR_UNSUPPORTED, "%s: head dim %d (a multiple of 16, at most 128)", who,
+      d);
+  REQ(scale_len == 16 || scale_len == 32 || scale_len == 64 || scale_len == 128, DLLM_ERR_UNSUPPORTED,
+      "%s: scale_len %d (16, 32, 64 or 128)", who, scale_len);
+  return DLLM_OK;
+}
+
+// What the two attention calls check alike; the largest launch grid is one CTA per 64 query rows of a (b, kv head), or
+// one per 32 keys.
+int check_attn_kv8(const char* who, int B, int Lq, int Hq, int Hkv, int d, int P, int cap, int scale_len, int dtype) {
+  REQ(B >= 1 && Lq >= 1 && Hq >= 1 && Hkv >= 1 && P >= 0, DLLM_ERR_SHAPE, "%s: non-positive dimension", who);
+  REQ(Hq % Hkv == 0, DLLM_ERR_SHAPE, "%s: Hq must be a multiple of Hkv", who);
+  REQ(cap >= P, DLLM_ERR_SHAPE, "%s: cap %d < P %d", who, cap, P);
+  REQ(dtype == DLLM_BF16 || dtype == DLLM_F32, DLLM_ERR_INVALID_ARG, "%s: bad dtype %d", who, dtype);
+  const int st = check_kv8_format(who, d, scale_len);
+  if (st) return st;
+  REQ(dtype == DLLM_F32 || d == 128, DLLM_ERR_UNSUPPORTED, "%s: bf16 needs head dim 128", who);
+  REQ((int64_t)Lq * (Hq / Hkv) <= (1 << 24) && (int64_t)B * Hkv * ((int64_t)Lq * (Hq / Hkv) / 64 + 1) <= (1 << 24) &&
+          (int64_t)B * Hkv * ((int64_t)P / 32 + 1) <= (1 << 30) && P <= (1 << 30),
+      DLLM_ERR_UNSUPPORTED, "%s: too many rows or keys for one call", who);
+  return DLLM_OK;
+}
+
+}  // namespace
+
+int dllm_kv8_store(const dllm_kv8_store_desc* d, const void* k, const void* v, const int32_t* src_pos,
+                   const int32_t* dst_rows, void* k_codes, void* v_codes, float* k_scale, float* v_scale,
+                   cudaStream_t stream) {
+  REQ(d && k && v && k_codes && v_codes && k_scale && v_scale, DLLM_ERR_INVALID_ARG, "kv8_store: NULL argument");
+  REQ(d->B >= 1 && d->Hkv >= 1 && d->n >= 0 && d->cap_src >= 1 && d->cap >= 1, DLLM_ERR_SHAPE,
+      "kv8_store: non-positive dimension");
+  REQ(d->dtype == DLLM_BF16 || d->dtype == DLLM_F32, DLLM_ERR_INVALID_ARG, "kv8_store: bad dtype %d", d->dtype);
+  int st = check_kv8_format("kv8_store", d->d, d->scale_len);
+  if (st) return st;
+  REQ(d->n <= d->cap, DLLM_ERR_SHAPE, "kv8_store: %d rows do not fit a cache of %d", d->n, d->cap);
+  if (src_pos)
+    REQ(d->pos_stride >= d->n, DLLM_ERR_SHAPE, "kv8_store: pos_stride %d < n %d", d->pos_stride, d->n);
+  else
+    REQ(d->src_row >= 0 && d->src_row <= d->cap_src - d->n, DLLM_ERR_SHAPE,
+        "kv8_store: source rows [%d, +%d) outside [0, %d)", d->src_row, d->n, d->cap_src);
+  if (!dst_rows) {
+    REQ(d->dst_row >= 0 && d->dst_row <= d->cap - d->n, DLLM_ERR_SHAPE,
+        "kv8_store: cache rows [%d, +%d) outside [0, %d)", d->dst_row, d->n, d->cap);
+    REQ(d->dst_row % d->scale_len == 0, DLLM_ERR_SHAPE, "kv8_store: dst_row %d does not start a run of %d", d->dst_row,
+        d->scale_len);
+  }
+  REQ((int64_t)d->B * d->Hkv * ((int64_t)d->n / d->scale_len + 1) <= (1 << 30), DLLM_ERR_UNSUPPORTED,
+      "kv8_store: too many rows for one call");
+  REQ(aligned16(k) && aligned16(v) && aligned16(k_codes) && aligned16(v_codes), DLLM_ERR_ALIGN,
+      "kv8_store: k, v and the code tensors must be 16-byte aligned");
+  if (d->n == 0) return DLLM_OK;
+  Kv8StoreArgs a;
+  a.B = d->B; a.Hkv = d->Hkv; a.d = d->d; a.n = d->n; a.cap_src = d->cap_src; a.src_row = d->src_row; a.cap = d->cap;
+  a.dst_row = d->dst_row; a.S = d->scale_len; a.dtype = d->dtype; a.pos_stride = d->pos_stride;
+  a.k = k; a.v = v; a.src_pos = src_pos; a.dst_rows = dst_rows;
+  a.k_codes = static_cast<uint8_t*>(k_codes); a.v_codes = static_cast<uint8_t*>(v_codes);
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  return launch_kv8_store(a, stream);
+}
+
+// Sizes are for both forms of the call, with and without own keys.
+size_t dllm_block_attn_kv8_workspace_size(const dllm_attn_kv8_desc* d) {
+  if (!d || d->B < 1 || d->Lq < 1 || d->Hkv < 1 || d->Hq < d->Hkv || d->P < 0) return 0;
+  return align256(kStatusBytes +
+                  std::max(attn_kv8_workspace_bytes(d->B, d->Lq, d->Hq, d->Hkv, d->d, d->P, 1, d->dtype),
+                           attn_kv8_workspace_bytes(d->B, d->Lq, d->Hq, d->Hkv, d->d, d->P, 0, d->dtype)));
+}
+
+int dllm_block_attn_kv8(const dllm_attn_kv8_desc* d, const void* q, const void* k_codes, const void* v_codes,
+                        const float* k_scale, const float* v_scale, const int32_t* prefix_len, const void* k_own,
+                        const void* v_own, void* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  REQ(d && q && out, DLLM_ERR_INVALID_ARG, "block_attn_kv8: NULL argument");
+  int st = check_attn_kv8("block_attn_kv8", d->B, d->Lq, d->Hq, d->Hkv, d->d, d->P, d->cap, d->scale_len, d->dtype);
+  if (st) return st;
+  REQ(d->P == 0 || (k_codes && v_codes && k_scale && v_scale), DLLM_ERR_INVALID_ARG, "block_attn_kv8: NULL cache");
+  REQ(d->blk_len >= 1, DLLM_ERR_SHAPE, "block_attn_kv8: blk_len %d", d->blk_len);
+  REQ((k_own == nullptr) == (v_own == nullptr), DLLM_ERR_INVALID_ARG,
+      "block_attn_kv8: k_own and v_own must both be set or both NULL");
+  REQ(!k_own || d->cap_own >= d->Lq, DLLM_ERR_SHAPE, "block_attn_kv8: cap_own %d < Lq %d", d->cap_own, d->Lq);
+  REQ(aligned16(q) && aligned16(out) && aligned16(k_codes) && aligned16(v_codes) && aligned16(k_own) &&
+          aligned16(v_own),
+      DLLM_ERR_ALIGN, "block_attn_kv8: q, out, codes and own rows must be 16-byte aligned");
+  const size_t qb = (size_t)d->B * d->Lq * d->Hq * d->d * esize(d->dtype);
+  REQ(!overlaps(q, qb, out, qb), DLLM_ERR_INVALID_ARG, "block_attn_kv8: out overlaps q");
+  st = check_ws(ws, ws_bytes, dllm_block_attn_kv8_workspace_size(d));
+  if (st) return st;
+  Carver c(ws);
+  Kv8AttnArgs a = {};
+  a.B = d->B; a.Lq = d->Lq; a.Hq = d->Hq; a.Hkv = d->Hkv; a.d = d->d; a.blk_len = d->blk_len; a.P = d->P;
+  a.cap = d->cap; a.cap_own = d->cap_own; a.S = d->scale_len; a.dtype = d->dtype;
+  a.scale = d->scale > 0.f ? d->scale : 1.0f / sqrtf((float)d->d);
+  a.q = q; a.k_codes = static_cast<const uint8_t*>(k_codes); a.v_codes = static_cast<const uint8_t*>(v_codes);
+  a.k_scale = k_scale; a.v_scale = v_scale; a.lens = prefix_len; a.k_own = k_own; a.v_own = v_own; a.out = out;
+  a.lse_out = lse; a.ws = c.take(0); a.status = status_word(ws);
+  return launch_attn_kv8(a, stream);
+}
+
+size_t dllm_attn_mass_kv8_workspace_size(const dllm_attn_mass_desc* d) { return d ? align256(kStatusBytes) : 0; }
+
+int dllm_attn_mass_kv8(const dllm_attn_mass_desc* d, const void* q, const void* k_codes, const float* k_scale,
+                       const int32_t* prefix_len, const float* lse, const float* mass_in, float* mass_out, void* ws,
+                       size_t ws_bytes, cudaStream_t stream) {
+  REQ(d && q && lse && mass_out, DLLM_ERR_INVALID_ARG, "attn_mass_kv8: NULL argument");
+  int st = check_attn_kv8("attn_mass_kv8", d->B, d->Lq, d->Hq, d->Hkv, d->d, d->P, d->cap, d->scale_len, d->dtype);
+  if (st) return st;
+  REQ(d->P == 0 || (k_codes && k_scale), DLLM_ERR_INVALID_ARG, "attn_mass_kv8: NULL cache");
+  REQ(aligned16(q) && aligned16(k_codes), DLLM_ERR_ALIGN, "attn_mass_kv8: q and codes must be 16-byte aligned");
+  const size_t mb = (size_t)d->B * d->Hkv * d->cap * 4;
+  REQ(mass_in == mass_out || !overlaps(mass_in, mb, mass_out, mb), DLLM_ERR_INVALID_ARG,
+      "attn_mass_kv8: mass_in and mass_out overlap in part");
+  st = check_ws(ws, ws_bytes, dllm_attn_mass_kv8_workspace_size(d));
+  if (st) return st;
+  if (d->P == 0) return DLLM_OK;
+  Kv8AttnArgs a = {};
+  a.B = d->B; a.Lq = d->Lq; a.Hq = d->Hq; a.Hkv = d->Hkv; a.d = d->d; a.blk_len = 1; a.P = d->P; a.cap = d->cap;
+  a.S = d->scale_len; a.dtype = d->dtype; a.scale = d->scale > 0.f ? d->scale : 1.0f / sqrtf((float)d->d);
+  a.q = q; a.k_codes = static_cast<const uint8_t*>(k_codes); a.k_scale = k_scale; a.lens = prefix_len;
+  a.lse_in = lse; a.mass_in = mass_in; a.mass_out = mass_out; a.decay = d->decay; a.status = status_word(ws);
+  return launch_attn_mass_kv8(a, stream);
+}
+
+size_t dllm_kv8_evict_workspace_size(const dllm_kv8_evict_desc* d) {
+  if (!d || d->B < 1 || d->Hkv < 1 || d->P < 0 || d->n_keep < 0) return 0;
+  return align256(kStatusBytes + kv8_evict_workspace_bytes(d->B, d->Hkv, d->P, d->n_keep, d->per_head));
+}
+
+int dllm_kv8_evict(const dllm_kv8_evict_desc* d, const void* k_codes, const void* v_codes, const float* k_scale,
+                   const float* v_scale, const float* mass, const int32_t* prefix_len, const int32_t* pos, void* k_out,
+                   void* v_out, float* k_scale_out, float* v_scale_out, float* mass_out, int32_t* keep_pos,
+                   int32_t* len_out, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  REQ(d && k_codes && v_codes && k_scale && v_scale && mass && k_out && v_out && k_scale_out && v_scale_out &&
+          mass_out && keep_pos && len_out,
+      DLLM_ERR_INVALID_ARG, "kv8_evict: NULL argument");
+  REQ(d->B >= 1 && d->Hkv >= 1 && d->P >= 0 && d->cap >= std::max(d->P, 1), DLLM_ERR_SHAPE, "kv8_evict: bad shape");
+  int st = check_kv8_format("kv8_evict", d->d, d->scale_len);
+  if (st) return st;
+  REQ(d->n_keep >= 1 && d->n_keep <= d->cap_out, DLLM_ERR_SHAPE, "kv8_evict: n_keep %d of cap_out %d", d->n_keep,
+      d->cap_out);
+  REQ(d->n_first >= 0 && d->n_last >= 0 && (int64_t)d->n_first + d->n_last <= d->n_keep, DLLM_ERR_INVALID_ARG,
+      "kv8_evict: n_first + n_last must be in [0, n_keep]");
+  REQ((int64_t)d->B * d->Hkv * ((int64_t)d->n_keep / d->scale_len + 1) <= (1 << 30) && d->P <= (1 << 30),
+      DLLM_ERR_UNSUPPORTED, "kv8_evict: too many rows for one call");
+  REQ(aligned16(k_codes) && aligned16(v_codes) && aligned16(k_out) && aligned16(v_out), DLLM_ERR_ALIGN,
+      "kv8_evict: code tensors must be 16-byte aligned");
+  {
+    const size_t bh = (size_t)d->B * d->Hkv, cb = bh * d->cap * d->d, co = bh * d->cap_out * d->d;
+    const size_t sb = bh * ((d->cap + d->scale_len - 1) / d->scale_len) * 4,
+                 so = bh * ((d->cap_out + d->scale_len - 1) / d->scale_len) * 4;
+    const size_t hs = (size_t)d->B * (d->per_head ? d->Hkv : 1);
+    const void* in[7] = {k_codes, v_codes, k_scale, v_scale, mass, pos, prefix_len};
+    const size_t nin[7] = {cb, cb, sb, sb, bh * d->cap * 4, hs * d->cap * 4, (size_t)d->B * 4};
+    const void* out[7] = {k_out, v_out, k_scale_out, v_scale_out, mass_out, keep_pos, len_out};
+    const size_t nout[7] = {co, co, so, so, bh * d->cap_out * 4, hs * d->cap_out * 4, (size_t)d->B * 4};
+    for (int i = 0; i < 7; ++i)
+      for (int j = 0; j < 7; ++j)
+        REQ(!overlaps(in[i], nin[i], out[j], nout[j]), DLLM_ERR_INVALID_ARG, "kv8_evict: an output overlaps an input");
+  }
+  st = check_ws(ws, ws_bytes, dllm_kv8_evict_workspace_size(d));
+  if (st) return st;
+  Carver c(ws);
+  Kv8EvictArgs a;
+  a.B = d->B; a.Hkv = d->Hkv; a.d = d->d; a.P = d->P; a.cap = d->cap; a.n_keep = d->n_keep; a.cap_out = d->cap_out;
+  a.S = d->scale_len; a.n_first = d->n_first; a.n_last = d->n_last; a.per_head = d->per_head != 0;
+  a.k_codes = static_cast<const uint8_t*>(k_codes); a.v_codes = static_cast<const uint8_t*>(v_codes);
+  a.k_scale = k_scale; a.v_scale = v_scale; a.mass = mass; a.lens = prefix_len; a.pos = pos;
+  a.k_out = static_cast<uint8_t*>(k_out); a.v_out = static_cast<uint8_t*>(v_out);
+  a.k_scale_out = k_scale_out; a.v_scale_out = v_scale_out; a.mass_out = mass_out; a.keep_pos = keep_pos;
+  a.len_out = len_out; a.ws = c.take(0);
+  return launch_kv8_evict(a, stream);
 }
 
 // ------------------------------------------------------------------------------------------------ router

@@ -1,0 +1,305 @@
+// The 8-bit KV cache's data movement: quantising K/V rows into it, and evicting its least attended positions.
+//
+// Format: E4M3 codes [B, Hkv, cap, d] and one fp32 scale per run of S tokens and kv head. The scale is the least
+// power of two that brings the run's largest magnitude to at most 448, so x / scale is exact and each value is rounded
+// once, to four significant bits (E4M3, nearest even): half a step is 2^-4 of the value, whatever the scale, so a
+// power of two costs no precision against amax / 448, and it lets eviction move rows between runs without rounding
+// them again.
+#include "kv8.cuh"
+#include "kv8.h"
+#include "misc.h"
+
+namespace dllm {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------------------------------------ store
+// A group of TG threads quantises one run (up to S rows of d elements): its vectors are read once, kept in registers
+// while the group's largest magnitude is found, then written as codes. TG = 2 S gives a thread at most VPT = 8
+// 16-byte vectors of bf16 (16 of fp32) at d = 128.
+template <typename T, int TG, int VPT>
+__global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs a, int runs) {
+  pdl_enter();
+  constexpr int VE = 16 / (int)sizeof(T);
+  __shared__ float red[kThreads / 32];
+  const int tid = threadIdx.x, gt = tid % TG;
+  const int64_t unit = (int64_t)blockIdx.x * (kThreads / TG) + tid / TG;
+  const bool is_v = blockIdx.y != 0;
+  const bool live = unit < (int64_t)a.B * a.Hkv * runs;
+  const int run = live ? (int)(unit % runs) : 0;
+  const int64_t bh = live ? unit / runs : 0;
+  const int b = (int)(bh / a.Hkv);
+  const int row0 = a.dst_rows ? a.dst_rows[b] : a.dst_row;
+  // a destination outside the cache or inside a run: nothing is written for this batch row
+  const bool ok = live && row0 >= 0 && row0 % a.S == 0 && row0 <= a.cap - a.n;
+  const int t0 = run * a.S, rows = min(a.S, a.n - t0);
+  const int vpr = a.d / VE;                       // vectors per row
+  const int nvec = ok ? rows * vpr : 0;
+  const T* src = static_cast<const T*>(is_v ? a.v : a.k) + bh * (int64_t)a.cap_src * a.d;
+  uint4 vec[VPT];
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int id = gt + i * TG;
+    vec[i] = make_uint4(0, 0, 0, 0);
+    if (id < nvec) {
+      const int r = id / vpr, c = id - r * vpr;
+      int row = a.src_row + t0 + r;
+      if (a.src_pos) row = a.src_pos[(int64_t)b * a.pos_stride + t0 + r];
+      if (row >= 0 && row < a.cap_src) vec[i] = ld_nc_v4(src + (int64_t)row * a.d + (int64_t)c * VE);
+    }
+  }
+  auto values = [&](const uint4& u, float* f) {
+    if constexpr (sizeof(T) == 2) {
+      bf16x8_to_f32(u, f);
+    } else {
+      f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
+      f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    float f[VE];
+    values(vec[i], f);
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      const float m = fabsf(f[j]);
+      if (m < INFINITY) amax = fmaxf(amax, m);     // infinities saturate, NaN stays NaN
+    }
+  }
+  amax = warp_max(amax);
+  if constexpr (TG > 32) {
+    if ((tid & 31) == 0) red[tid >> 5] = amax;
+    __syncthreads();
+    const int w0 = tid / TG * (TG / 32);
+#pragma unroll
+    for (int w = 0; w < TG / 32; ++w) amax = fmaxf(amax, red[w0 + w]);
+  }
+  if (!ok) return;
+  const int k = kv8::scale_exp(amax);
+  const float inv = kv8::exp2i(-k);
+  uint8_t* dst = (is_v ? a.v_codes : a.k_codes) + (bh * (int64_t)a.cap + row0 + t0) * a.d;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int id = gt + i * TG;
+    if (id < nvec) {
+      float f[VE];
+      values(vec[i], f);
+      uint32_t w[VE / 4];
+#pragma unroll
+      for (int j = 0; j < VE / 4; ++j)
+        w[j] = kv8::f32x2_to_e4m3x2(f[4 * j] * inv, f[4 * j + 1] * inv) |
+               (kv8::f32x2_to_e4m3x2(f[4 * j + 2] * inv, f[4 * j + 3] * inv) << 16);
+      // the run's rows are contiguous, so vector id of the source lands at id * VE codes
+      if constexpr (VE == 8)
+        *reinterpret_cast<uint2*>(dst + (int64_t)id * 8) = make_uint2(w[0], w[1]);
+      else
+        *reinterpret_cast<uint32_t*>(dst + (int64_t)id * 4) = w[0];
+    }
+  }
+  if (gt == 0) {
+    const int n_runs = (a.cap + a.S - 1) / a.S;
+    (is_v ? a.v_scale : a.k_scale)[bh * n_runs + row0 / a.S + run] = kv8::exp2i(k);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------ evict
+// Ordered key of a position: the bits of its accumulated weight (non-negative, so bit order is value order; NaN and
+// negative values count as 0), above every weight for the positions that are always kept.
+constexpr uint32_t kForced = 0x7f800001u;
+
+// One CTA per selection (batch row, or batch row and kv head): keys, the n_keep-th largest key by a radix search
+// over bytes, then the kept positions in increasing order (equal keys at the threshold: the lower position first).
+__global__ void __launch_bounds__(1024) kv8_select_kernel(const Kv8EvictArgs a, uint32_t* __restrict__ keys,
+                                                          int32_t* __restrict__ index) {
+  pdl_enter();
+  __shared__ unsigned hist[256];
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_need;
+  __shared__ int wsum[32];
+  const int sel = blockIdx.x, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int Hs = a.per_head ? a.Hkv : 1;
+  const int b = sel / Hs, h = sel - b * Hs;
+  const int len = kv8::prefix_len(a.lens, b, a.P);
+  const int keep = min(len, a.n_keep);
+  uint32_t* key = keys + (int64_t)sel * a.P;
+  if (h == 0 && tid == 0) a.len_out[b] = keep;
+  for (int j = tid; j < len; j += 1024) {
+    // the heads' weights are summed in 64 bits, in head order
+    double t = 0.0;
+    if (a.per_head) {
+      t = a.mass[((int64_t)b * a.Hkv + h) * a.cap + j];
+    } else {
+      for (int g = 0; g < a.Hkv; ++g) t += (double)a.mass[((int64_t)b * a.Hkv + g) * a.cap + j];
+    }
+    const float f = (float)t;
+    key[j] = (j < a.n_first || j >= len - a.n_last) ? kForced : __float_as_uint(f > 0.f ? f : 0.f);
+  }
+  uint32_t prefix = 0, mask = 0;
+  int need = keep;      // how many of the keys that match the prefix are still to be taken
+  __syncthreads();
+  for (int shift = 24; shift >= 0 && keep > 0 && keep < len; shift -= 8) {
+    if (tid < 256) hist[tid] = 0;
+    __syncthreads();
+    for (int j = tid; j < len; j += 1024) {
+      const uint32_t u = key[j];
+      if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1u);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      int left = need, bin = 255;
+      while (bin > 0 && (int)hist[bin] < left) left -= (int)hist[bin--];
+      s_need = left;
+      s_prefix = prefix | ((uint32_t)bin << shift);
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    need = s_need;
+    mask |= 255u << shift;
+  }
+  // prefix is now the threshold: larger keys are kept, and the first `need` equal ones
+  const bool all = keep == len;
+  int base = 0, base_eq = 0;
+  const int32_t* pos = a.pos ? a.pos + (int64_t)sel * a.cap : nullptr;
+  for (int j0 = 0; j0 < len; j0 += 1024) {
+    const int j = j0 + tid;
+    const uint32_t u = j < len ? key[j] : 0u;
+    const bool eq = j < len && !all && u == prefix;
+    bool take = j < len && (all || u > prefix);
+    // rank among the equal keys, then rank among the kept positions
+    for (int pass = 0; pass < 2; ++pass) {
+      const unsigned bal = __ballot_sync(0xffffffffu, pass == 0 ? eq : take);
+      __syncthreads();
+      if (lane == 0) wsum[w] = __popc(bal);
+      __syncthreads();
+      int before = 0, total = 0;
+      for (int k = 0; k < 32; ++k) {
+        before += k < w ? wsum[k] : 0;
+        total += wsum[k];
+      }
+      const int rank = before + __popc(bal & ((1u << lane) - 1u));
+      if (pass == 0) {
+        take |= eq && base_eq + rank < need;
+        base_eq += total;
+      } else {
+        if (take) {
+          index[(int64_t)sel * a.n_keep + base + rank] = j;
+          a.keep_pos[(int64_t)sel * a.cap_out + base + rank] = pos ? pos[j] : j;
+        }
+        base += total;
+      }
+    }
+  }
+}
+
+// A group of TG = 2 S threads moves one run of S kept rows of a (batch row, kv head): K and V codes and the
+// accumulated weights. The run's scale is the largest of its rows' scales; a row whose scale is smaller has its codes
+// multiplied by the ratio and rounded again, which for power-of-two scales changes only values below 2^-6 of the new
+// scale (E4M3's subnormals).
+template <int TG>
+__global__ void __launch_bounds__(kThreads) kv8_gather_kernel(const Kv8EvictArgs a, const int32_t* __restrict__ index,
+                                                              int runs) {
+  pdl_enter();
+  constexpr int S = TG / 2, GROUPS = kThreads / TG;
+  __shared__ int src_s[GROUPS][S];
+  __shared__ float sc_s[GROUPS][2][S];
+  const int tid = threadIdx.x, gt = tid % TG, grp = tid / TG;
+  const int64_t unit = (int64_t)blockIdx.x * GROUPS + grp;
+  const bool live = unit < (int64_t)a.B * a.Hkv * runs;
+  const int run = live ? (int)(unit % runs) : 0;
+  const int64_t bh = live ? unit / runs : 0;
+  const int b = (int)(bh / a.Hkv);
+  const int keep = min(kv8::prefix_len(a.lens, b, a.P), a.n_keep);
+  const int t0 = run * S, rows = live ? min(S, keep - t0) : 0;
+  const int64_t sel = a.per_head ? bh : b;
+  const int64_t runs_in = (a.cap + S - 1) / S, runs_out = (a.cap_out + S - 1) / S;
+  if (gt < rows) {
+    const int j = index[sel * a.n_keep + t0 + gt];
+    src_s[grp][gt] = j;
+    sc_s[grp][0][gt] = a.k_scale[bh * runs_in + j / S];
+    sc_s[grp][1][gt] = a.v_scale[bh * runs_in + j / S];
+    a.mass_out[bh * (int64_t)a.cap_out + t0 + gt] = a.mass[bh * (int64_t)a.cap + j];
+  }
+  __syncthreads();
+  if (rows <= 0) return;
+  const int vpr = a.d / 16, nvec = rows * vpr;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    float top = 0.f;
+    for (int r = 0; r < rows; ++r) top = fmaxf(top, sc_s[grp][kv][r]);
+    const uint8_t* src = (kv ? a.v_codes : a.k_codes) + bh * (int64_t)a.cap * a.d;
+    uint8_t* dst = (kv ? a.v_out : a.k_out) + (bh * (int64_t)a.cap_out + t0) * a.d;
+    for (int id = gt; id < nvec; id += TG) {
+      const int r = id / vpr, c = id - r * vpr;
+      uint4 u = ld_nc_v4(src + (int64_t)src_s[grp][r] * a.d + c * 16);
+      const float old = sc_s[grp][kv][r];
+      if (old != top) {
+        const float ratio = top > 0.f ? old / top : 0.f;
+        float f[16];
+        kv8::codes16_to_f32(u, f);
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          o[i] = kv8::f32x2_to_e4m3x2(f[4 * i] * ratio, f[4 * i + 1] * ratio) |
+                 (kv8::f32x2_to_e4m3x2(f[4 * i + 2] * ratio, f[4 * i + 3] * ratio) << 16);
+        u = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      *reinterpret_cast<uint4*>(dst + (int64_t)id * 16) = u;
+    }
+    if (gt == 0) (kv ? a.v_scale_out : a.k_scale_out)[bh * runs_out + run] = top;
+  }
+}
+
+}  // namespace
+
+int launch_kv8_store(const Kv8StoreArgs& a, cudaStream_t s) {
+  const int runs = (a.n + a.S - 1) / a.S;
+  const int64_t units = (int64_t)a.B * a.Hkv * runs;
+  const int per = kThreads / (2 * a.S);
+  const dim3 grid((unsigned)((units + per - 1) / per), 2);
+#define DLLM_STORE(T, V)                                                                        \
+  switch (a.S) {                                                                                \
+    case 16: launch_pdl(kv8_store_kernel<T, 32, V>, grid, kThreads, 0, s, a, runs); break;      \
+    case 32: launch_pdl(kv8_store_kernel<T, 64, V>, grid, kThreads, 0, s, a, runs); break;      \
+    case 64: launch_pdl(kv8_store_kernel<T, 128, V>, grid, kThreads, 0, s, a, runs); break;     \
+    default: launch_pdl(kv8_store_kernel<T, 256, V>, grid, kThreads, 0, s, a, runs); break;     \
+  }
+  if (a.dtype == DLLM_BF16) {
+    DLLM_STORE(__nv_bfloat16, 8)
+  } else {
+    DLLM_STORE(float, 16)
+  }
+#undef DLLM_STORE
+  DLLM_CHECK_LAUNCH("kv8_store_kernel");
+  return DLLM_OK;
+}
+
+size_t kv8_evict_workspace_bytes(int B, int Hkv, int P, int n_keep, int per_head) {
+  const size_t sel = (size_t)B * (per_head ? Hkv : 1);
+  return (sel * P * 4 + 255) / 256 * 256 + sel * n_keep * 4;
+}
+
+int launch_kv8_evict(const Kv8EvictArgs& a, cudaStream_t s) {
+  const int64_t sel = (int64_t)a.B * (a.per_head ? a.Hkv : 1);
+  uint32_t* keys = static_cast<uint32_t*>(a.ws);
+  int32_t* index = reinterpret_cast<int32_t*>(static_cast<char*>(a.ws) + ((size_t)sel * a.P * 4 + 255) / 256 * 256);
+  launch_pdl(kv8_select_kernel, (unsigned)sel, 1024, 0, s, a, keys, index);
+  DLLM_CHECK_LAUNCH("kv8_select_kernel");
+  const int most = min(a.n_keep, a.P);
+  if (most == 0) return DLLM_OK;
+  const int runs = (most + a.S - 1) / a.S;
+  const int64_t units = (int64_t)a.B * a.Hkv * runs;
+  const int per = kThreads / (2 * a.S);
+  const unsigned grid = (unsigned)((units + per - 1) / per);
+  switch (a.S) {
+    case 16: launch_pdl(kv8_gather_kernel<32>, grid, kThreads, 0, s, a, (const int32_t*)index, runs); break;
+    case 32: launch_pdl(kv8_gather_kernel<64>, grid, kThreads, 0, s, a, (const int32_t*)index, runs); break;
+    case 64: launch_pdl(kv8_gather_kernel<128>, grid, kThreads, 0, s, a, (const int32_t*)index, runs); break;
+    default: launch_pdl(kv8_gather_kernel<256>, grid, kThreads, 0, s, a, (const int32_t*)index, runs); break;
+  }
+  DLLM_CHECK_LAUNCH("kv8_gather_kernel");
+  return DLLM_OK;
+}
+
+}  // namespace dllm

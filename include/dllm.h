@@ -441,6 +441,116 @@ typedef struct {
 DLLM_API int dllm_denoise_step_views(const dllm_model* model, const dllm_state* state, const dllm_step_params* params,
                             void* ws, size_t ws_bytes, dllm_step_views* views /* host */);
 
+/* ---------------------------------------------------------------------------------------------- B8 8-bit KV cache */
+/*
+ * A KV cache in 8 bits, for the prefix that every denoising pass of a block reads again ([M] "SPRINT 加速技术": the
+ * prefix KV is computed once and reused; the pages describe no 8-bit cache, the format is this library's):
+ *   k_codes, v_codes  [B, Hkv, cap, d]  OCP E4M3 codes, one byte each (keys already rotated by RoPE)
+ *   k_scale, v_scale  [B, Hkv, ceil(cap / scale_len)] fp32: one positive finite scale for each run of scale_len tokens
+ *                     of a kv head; the value of a code is value(code) * scale
+ * scale_len is 16, 32, 64 or 128. Code tensors are 16-byte aligned and d is a multiple of 16, at most 128.
+ *
+ * dllm_kv8_store quantises n rows of K and V of every (row, kv head) into it. The scale of a run is 2^k, k the least
+ * integer for which its largest finite magnitude is at most 448 * 2^k, limited to -64 <= k <= 120; every value is
+ * divided by it (exactly) and rounded once to E4M3, nearest even. Infinities become +-448 times the scale, NaN stays
+ * NaN.
+ *   k, v      [B, Hkv, cap_src, d] in the storage type, 16-byte aligned; token t is row src_row + t
+ *   src_pos   [B, pos_stride] int32 (nullable): token t of batch row b is source row src_pos[b, t] instead (a position
+ *             list as dllm_prefix_retain writes it); positions outside [0, cap_src) are stored as zeros
+ *   dst_rows  [B] int32 (nullable): first cache row written of each batch row, dst_row for all without it. It starts a
+ *             run (a multiple of scale_len) and leaves room for n rows; a batch row whose device value does not is
+ *             left as it was. The last run may end early: its other rows keep their codes.
+ */
+typedef struct {
+  int32_t B, Hkv, d, n;
+  int32_t cap_src, src_row;
+  int32_t cap, dst_row;
+  int32_t scale_len;
+  int32_t dtype;
+  int32_t pos_stride;
+} dllm_kv8_store_desc;
+DLLM_API int dllm_kv8_store(const dllm_kv8_store_desc* desc, const void* k, const void* v, const int32_t* src_pos,
+                            const int32_t* dst_rows, void* k_codes, void* v_codes, float* k_scale, float* v_scale,
+                            cudaStream_t stream);
+
+/*
+ * dllm_block_attn over an 8-bit prefix of each row's own length and the queries' own K/V in the storage type:
+ * query i of row b sees the prefix rows j < prefix_len[b] and its own rows j with floor(j / blk_len) <=
+ * floor(i / blk_len) (blk_len >= Lq: the block's bidirectional attention; 1: causal tokens), softmax over both.
+ *   q            [B, Lq, Hq, d], 16-byte aligned
+ *   prefix_len   [B] int32 (nullable: P for every row), read clamped to [0, P]; rows past it may hold anything
+ *   k_own, v_own [B, Hkv, cap_own, d] in the storage type, rows [0, Lq) (both NULL: the prefix only)
+ *   out          [B, Lq, Hq * d], 16-byte aligned; zeros where a query sees no key
+ *   lse          [B, Lq, Hq] fp32 (nullable): log of the sum of exp(score) over the query's keys, -inf without keys
+ * scale <= 0 selects 1/sqrt(d). Any Hq a multiple of Hkv. bf16: d == 128. Own V rows must be finite (a query's weight
+ * on a row it does not see is 0, and 0 times infinity is not); V scales below 2^-64 are read as 2^-64.
+ */
+typedef struct {
+  int32_t B, Lq, Hq, Hkv, d;
+  int32_t blk_len;
+  int32_t P, cap;
+  int32_t cap_own;
+  int32_t scale_len;
+  int32_t dtype;
+  float scale;
+} dllm_attn_kv8_desc;
+DLLM_API int dllm_block_attn_kv8(const dllm_attn_kv8_desc* desc, const void* q, const void* k_codes,
+                                 const void* v_codes, const float* k_scale, const float* v_scale,
+                                 const int32_t* prefix_len, const void* k_own, const void* v_own, void* out, float* lse,
+                                 void* ws, size_t ws_bytes, cudaStream_t stream);
+DLLM_API size_t dllm_block_attn_kv8_workspace_size(const dllm_attn_kv8_desc* desc);
+
+/*
+ * The attention weight that the queries put on every prefix row, added to an accumulator per kv head:
+ *   mass_out[b, h, j] = decay * mass_in[b, h, j] + sum over the queries i and the query heads g of kv head h of
+ *                       exp(score(i, g, j) - lse[b, i, g]),   j < prefix_len[b]
+ * with the lse that dllm_block_attn_kv8 wrote for the same queries (rows of lse -inf add nothing). Sums in a fixed
+ * order: the same inputs give the same bits.
+ *   mass_in (nullable: zeros), mass_out [B, Hkv, cap] fp32, the same array or disjoint ones; rows past a prefix are
+ *   left as they were.
+ */
+typedef struct {
+  int32_t B, Lq, Hq, Hkv, d;
+  int32_t P, cap;
+  int32_t scale_len;
+  int32_t dtype;
+  float scale;
+  float decay;
+} dllm_attn_mass_desc;
+DLLM_API int dllm_attn_mass_kv8(const dllm_attn_mass_desc* desc, const void* q, const void* k_codes,
+                                const float* k_scale, const int32_t* prefix_len, const float* lse,
+                                const float* mass_in, float* mass_out, void* ws, size_t ws_bytes, cudaStream_t stream);
+DLLM_API size_t dllm_attn_mass_kv8_workspace_size(const dllm_attn_mass_desc* desc);
+
+/*
+ * Eviction by accumulated attention weight: of every row's prefix the first n_first and the last n_last rows are kept
+ * and of the others those with the largest weight (summed over the kv heads in 64 bits and rounded to fp32; equal
+ * weights: the lower row; NaN and negative weights count as 0), min(n_keep, prefix_len[b]) rows in all. They are
+ * written in increasing order to rows [0, len_out[b]) of another 8-bit cache with the same scale_len, together with
+ * their accumulators. per_head != 0: every kv head keeps rows of its own, by its own weights.
+ * A run's new scale is the largest among its rows; codes of rows with a smaller one are multiplied by the ratio and
+ * rounded to E4M3 (for power-of-two scales exact but for values below 2^-6 of the new scale).
+ *   mass      [B, Hkv, cap] fp32
+ *   pos       [B, per_head ? Hkv : 1, cap] int32 (nullable): the rows' positions, their row numbers without it
+ *   k_out, v_out [B, Hkv, cap_out, d]; k_scale_out, v_scale_out [B, Hkv, ceil(cap_out / scale_len)]; mass_out [B, Hkv,
+ *   cap_out]; keep_pos [B, per_head ? Hkv : 1, cap_out] int32: the kept rows' positions; len_out [B] int32.
+ * Rows past len_out are left as they were. No output overlaps an input. n_first + n_last <= n_keep <= cap_out.
+ */
+typedef struct {
+  int32_t B, Hkv, d;
+  int32_t P, cap;
+  int32_t n_keep, cap_out;
+  int32_t scale_len;
+  int32_t n_first, n_last;
+  int32_t per_head;
+} dllm_kv8_evict_desc;
+DLLM_API int dllm_kv8_evict(const dllm_kv8_evict_desc* desc, const void* k_codes, const void* v_codes,
+                            const float* k_scale, const float* v_scale, const float* mass, const int32_t* prefix_len,
+                            const int32_t* pos, void* k_out, void* v_out, float* k_scale_out, float* v_scale_out,
+                            float* mass_out, int32_t* keep_pos, int32_t* len_out, void* ws, size_t ws_bytes,
+                            cudaStream_t stream);
+DLLM_API size_t dllm_kv8_evict_workspace_size(const dllm_kv8_evict_desc* desc);
+
 #ifdef __cplusplus
 }
 #endif
