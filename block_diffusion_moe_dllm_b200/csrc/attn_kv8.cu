@@ -328,9 +328,8 @@ template <typename T>
 static int run_simt(const Kv8AttnArgs& a, cudaStream_t s) {
   const SimtPlan p = simt_plan(a.B, a.Lq, a.Hq, a.Hkv, a.P, a.k_own != nullptr);
   const size_t smem = ((size_t)(ROWS + 2 * KB) * (a.d + 4) + ROWS * PD) * 4;
-  static const cudaError_t e = cudaFuncSetAttribute(attn_kv8_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    ((ROWS + 2 * KB) * 132 + ROWS * PD) * 4);
-  if (e != cudaSuccess) return dllm_host::cuda_status(e, "cudaFuncSetAttribute(attn_kv8_simt)");
+  const int st = set_max_smem<attn_kv8_simt_kernel<T>>(((ROWS + 2 * KB) * 132 + ROWS * PD) * 4);
+  if (st) return st;
   float* part = static_cast<float*>(a.ws);
   launch_pdl(attn_kv8_simt_kernel<T>, dim3((unsigned)(a.B * a.Hkv * p.n_rt), p.n_splits), 256, smem, s, a, p, part);
   DLLM_CHECK_LAUNCH("attn_kv8_simt_kernel");
@@ -351,16 +350,12 @@ int launch_attn_mass_kv8_simt(const Kv8AttnArgs& a, cudaStream_t s) {
   const size_t smem = ((size_t)(ROWS + KB) * (a.d + 4) + 16 * KB) * 4;
   const unsigned grid = (unsigned)((int64_t)a.B * a.Hkv * n_kt);
   if (a.dtype == DLLM_BF16) {
-    static const cudaError_t e = cudaFuncSetAttribute(attn_mass_kv8_simt_kernel<__nv_bfloat16>,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                      ((ROWS + KB) * 132 + 16 * KB) * 4);
-    if (e != cudaSuccess) return dllm_host::cuda_status(e, "cudaFuncSetAttribute(attn_mass_kv8_simt)");
+    const int st = set_max_smem<attn_mass_kv8_simt_kernel<__nv_bfloat16>>(((ROWS + KB) * 132 + 16 * KB) * 4);
+    if (st) return st;
     launch_pdl(attn_mass_kv8_simt_kernel<__nv_bfloat16>, grid, 256, smem, s, a, n_kt, n_rt);
   } else {
-    static const cudaError_t e = cudaFuncSetAttribute(attn_mass_kv8_simt_kernel<float>,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                      ((ROWS + KB) * 132 + 16 * KB) * 4);
-    if (e != cudaSuccess) return dllm_host::cuda_status(e, "cudaFuncSetAttribute(attn_mass_kv8_simt)");
+    const int st = set_max_smem<attn_mass_kv8_simt_kernel<float>>(((ROWS + KB) * 132 + 16 * KB) * 4);
+    if (st) return st;
     launch_pdl(attn_mass_kv8_simt_kernel<float>, grid, 256, smem, s, a, n_kt, n_rt);
   }
   DLLM_CHECK_LAUNCH("attn_mass_kv8_simt_kernel");
@@ -368,10 +363,12 @@ int launch_attn_mass_kv8_simt(const Kv8AttnArgs& a, cudaStream_t s) {
 }
 
 size_t attn_kv8_workspace_bytes(int B, int Lq, int Hq, int Hkv, int d, int P, int own, int dtype) {
-  (void)dtype;
+  if (dtype == DLLM_BF16) return attn_kv8_tc_workspace_bytes(B, Lq, Hq, Hkv);
   return attn_kv8_simt_workspace_bytes(B, Lq, Hq, Hkv, d, P, own);
 }
-int launch_attn_kv8(const Kv8AttnArgs& a, cudaStream_t s) { return launch_attn_kv8_simt(a, s); }
+int launch_attn_kv8(const Kv8AttnArgs& a, cudaStream_t s) {
+  return a.dtype == DLLM_BF16 ? launch_attn_kv8_tc(a, s) : launch_attn_kv8_simt(a, s);
+}
 int launch_attn_mass_kv8(const Kv8AttnArgs& a, cudaStream_t s) { return launch_attn_mass_kv8_simt(a, s); }
 
 }  // namespace dllm

@@ -1,0 +1,942 @@
+// Attention over an 8-bit prefix cache and the block's own K/V on the 5th-generation tensor cores (tcgen05 + TMEM),
+// bf16 queries, head dim 128. The formulas are in attn_kv8.cu.
+//
+// Work: the (query, head of the group) rows of a (batch row, kv head) are cut into tiles of 128 rows, each a unit of
+// ceil(len[b] / 128) prefix key tiles and the own key tiles its last query sees. All units' key tiles in a row are
+// dealt to one CTA per SM in equal contiguous shares, so rows of different lengths, few rows and many rows all keep
+// every SM on the same number of tiles; a unit that spans several CTAs leaves its partial results (unnormalised o, m, l
+// per row) in the workspace and a second kernel joins them.
+//
+// Per key tile of 128:
+//   S = Q K^T   kind::f8f6f4, K's codes straight from the cache by TMA (never converted). The queries are exact
+//               to 2^-17.8 of their row's largest magnitude as two E4M3 parts: q * 2^-k brought to at most 448, hi =
+//               E4M3(q), lo = E4M3(q - hi) (bf16 has 8 significant bits, two parts of 4); both parts accumulate into the
+//               same fp32 S. fp8 MMAs run at twice the bf16 rate, so the two cost what one bf16 product would.
+//               Own keys are split the same way by the converter warps (two parts with one power-of-two scale per tile:
+//               four products).
+//   softmax     one thread per row; x = S * (2^k scale log2(e) k_scale) + log2(v_scale) - m: the V scale of each run rides
+//               in the exponent, so that P V needs no scaled copy of V; the row sum divides it out again run by run.
+//               P = 2^(x + 6) as f16, with m within 2^8 of the true maximum: the largest weight is in [2^-2, 2^14] and a
+//               weight keeps 11 bits down to 2^-20 of it and is dropped below 2^-31.
+//   O += P V    kind::f16 with A = P from TMEM and B = V as f16 (every E4M3 value is one), written from the codes by four
+//               converter warps into the MN-major layout.
+// Tensor time of a tile: 8 + 8 MMAs of 64 clocks, and about 250 clocks for each of the two changes of the instruction
+// descriptor (measured on bare loops: 512 clocks per 8 MMAs of one kind, 756 when S and P V alternate, whatever their
+// operand sources), so about 1510 clocks, against 1420 for the tile's bytes at one SM's share of the HBM rate and 1024
+// for its exponentials. Three S buffers and one O in TMEM keep three tiles in flight, so that the tensor pipe does not
+// wait for a softmax; two threads share a row (columns [0, 64) and [64, 128) of every tile), whose common reference
+// maximum moves only when a tile exceeds it by 2^8: a vote of the row's two warps decides, and only then do they exchange
+// maxima and rescale O.
+//
+// Roles: warp 0 TMA, warp 1 MMA, warps 2 and 3 the runs' scales (alternate prefix tiles), warps 4-7 and 8-11 softmax (lower
+// and upper half of the columns), warps 12-15 convert Q, V and the own rows. Warps whose rows are all past the last only
+// keep count. Every wait is bounded; a wait that gives up sets the abort flag and the status word, after which every
+// role runs through its loops without waiting, issuing or storing anything.
+#include "attn_tc.cuh"
+#include "kv8.cuh"
+#include "kv8.h"
+#include "misc.h"
+#include <algorithm>
+
+namespace dllm {
+namespace {
+
+constexpr int NT = 512;
+constexpr int KT = 128;                    // keys per tile = rows per unit
+constexpr int KSTAGE = 128 * 128;          // K or V codes of a tile: 16 KB
+constexpr int VTILE = 2 * 128 * 64 * 2;    // V of a tile as f16: two 64-wide chunks of 16 KB
+constexpr int VCHUNK = VTILE / 2;
+constexpr int NK = 3, NV = 2, NB = 3;      // stages of the K and V code rings; S and f16 V buffers
+constexpr float kRescale = 8.f;            // the reference maximum moves when a tile exceeds it by 2^8
+constexpr float kOff = 6.f;                // P is 2^6 times the weight relative to the reference maximum
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kBarConv = 1, kBarPair = 2;  // named barriers: the 128 converter threads; 2 + i: the two warps of rows 32 i ..
+constexpr int kPart = 33 * 128 * 4;        // floats of one partial result: 32 float4 columns and (m, l, -, -), by row
+
+struct Bars {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[NK], k_empty[NK];
+  uint64_t k_grant[NK];                    // a free K stage handed to the converters, for own rows
+  uint64_t v_full[NV], v_empty[NV];
+  uint64_t w_full[NB], w_empty[NB];        // f16 V of a tile; empty = the tile's P V is complete
+  uint64_t s_full[NB], p_ready[NB];
+  uint64_t r_full[4], r_empty[4];          // scales of a prefix tile
+  uint64_t o_free;                         // O of the finished unit has been read
+  uint64_t done;
+  uint32_t tmem_base;
+  int abort_flag;
+  int walk[6];                             // b, h, rt, first tile, number of tiles of this CTA; tiles of all CTAs
+  float red[2][4];                         // own rows' largest magnitudes, by converter warp
+  float qscale[KT];                        // per row: 2^k * scale * log2(e)
+  float4 run[4][8];                        // per prefix tile and 16 keys: k scale, log2(v scale), 1 / v scale
+  float4 run_own[NB];                      // of an own tile
+  float xm[2][2][KT], xl[2][2][KT];        // [parity][column half][row]: maxima, sums
+};
+constexpr int SMEM = 1024 + 2 * KSTAGE /*Q*/ + NK * KSTAGE + NV * KSTAGE + NB * VTILE + (int)sizeof(Bars);
+static_assert(SMEM <= 232448, "shared memory budget");
+static_assert(SMEM > 233472 / 2, "tensor-memory kernels must not share an SM");
+
+struct Params {
+  Kv8AttnArgs a;
+  int G, n_rows, n_rt;        // rows Lq * G of a (b, kv head), row tiles
+  int64_t own_sum;            // own key tiles of all row tiles of a (b, kv head)
+  int n_cta;
+  float* part;                // [n_cta][2][kPart]
+  int4* span;                 // [units]: first tile, CTAs that share the unit (0: one, already written), all tiles
+  int reuse;                  // several row tiles read the same keys: keep them in L2
+};
+
+// Own keys that rows of tile rt see (their last query's block).
+DLLM_DEV int own_keys(const Params& p, int rt) {
+  if (!p.a.k_own) return 0;
+  const int last_q = (min((rt + 1) * KT, p.n_rows) - 1) / p.G;
+  return (int)min((int64_t)p.a.Lq, ((int64_t)(last_q / p.a.blk_len) + 1) * p.a.blk_len);
+}
+DLLM_DEV int cdiv128(int x) { return (int)(((unsigned)x + 127u) >> 7); }
+// Key tiles of all units of batch row b: at least one per unit, so that rows without keys are written too.
+DLLM_DEV int64_t row_tiles(const Params& p, int b) {
+  const int tp = cdiv128(kv8::prefix_len(p.a.lens, b, p.a.P));
+  return (int64_t)p.a.Hkv * ((int64_t)p.n_rt * (p.a.k_own ? tp : max(tp, 1)) + p.own_sum);
+}
+
+// Position in the sequence of key tiles, advanced unit by unit; every role walks it by itself.
+struct Walk {
+  int b, h, rt, ta, n;      // unit, first tile in it, tiles left to this CTA
+  int len, tp, own, tiles;  // of the unit: prefix length, prefix tiles, own keys, all tiles
+  DLLM_DEV void unit(const Params& p, bool new_row) {
+    if (new_row) {
+      len = kv8::prefix_len(p.a.lens, b, p.a.P);
+      tp = cdiv128(len);
+    }
+    own = own_keys(p, rt);
+    tiles = max(1, tp + cdiv128(own));
+  }
+  DLLM_DEV void start(const Params& p, const int* w) {
+    b = w[0]; h = w[1]; rt = w[2]; ta = w[3]; n = w[4];
+    if (n > 0) unit(p, true);
+  }
+  DLLM_DEV int end() const { return min(tiles, ta + n); }    // the CTA's tiles of this unit: [ta, end())
+  DLLM_DEV void next(const Params& p) {
+    n -= end() - ta;
+    ta = 0;
+    bool row = false;
+    if (++rt == p.n_rt) {
+      rt = 0;
+      if (++h == p.a.Hkv) {
+        h = 0;
+        ++b;
+        row = true;
+      }
+    }
+    if (n > 0) unit(p, row);
+  }
+};
+
+// Tile x of the whole sequence as (b, h, rt, tile in the unit), by one warp; total_out: the number of all tiles.
+// first[3]: see find_unit's use in the merge.
+DLLM_DEV int64_t total_tiles(const Params& p) {
+  const int lane = threadIdx.x & 31;
+  if (!p.a.lens) return p.a.B * row_tiles(p, 0);
+  int64_t t = 0;
+  for (int b = lane; b < p.a.B; b += 32) t += row_tiles(p, b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t;
+}
+DLLM_DEV void locate(const Params& p, int64_t x, int& b, int& h, int& rt, int& ta) {
+  const int lane = threadIdx.x & 31;
+  int64_t rem = 0;
+  if (!p.a.lens) {
+    const int64_t per = row_tiles(p, 0);
+    b = (int)(x / per);
+    rem = x - b * per;
+  } else {
+    int64_t base = 0;
+    b = p.a.B - 1;
+    for (int b0 = 0; b0 < p.a.B; b0 += 32) {
+      int64_t v = b0 + lane < p.a.B ? row_tiles(p, b0 + lane) : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, base + v > x);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        const int64_t before = __shfl_sync(0xffffffffu, v, max(l - 1, 0));
+        b = b0 + l;
+        rem = x - base - (l > 0 ? before : 0);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  const int64_t per_h = row_tiles(p, b) / p.a.Hkv;
+  h = (int)(rem / per_h);
+  rem -= h * per_h;
+  const int tp = cdiv128(kv8::prefix_len(p.a.lens, b, p.a.P));
+  for (rt = 0; rt + 1 < p.n_rt; ++rt) {
+    const int t = max(1, tp + cdiv128(own_keys(p, rt)));
+    if (rem < t) break;
+    rem -= t;
+  }
+  ta = (int)rem;
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  uint32_t z = 0;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four threads quantise a row of 128 bf16 values into two E4M3 parts: this thread's quarter (32 values, src NULL: zeros).
+struct Quarter {
+  uint4 raw[4];
+  DLLM_DEV void load(const __nv_bfloat16* src) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[i] = src ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
+  }
+  // largest finite magnitude; bad: whether a value is infinite or NaN
+  DLLM_DEV float amax(bool& bad) const {
+    float m = 0.f;
+    bad = false;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float f[8];
+      bf16x8_to_f32(raw[g], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = fabsf(f[i]);
+        const bool fin = x < INFINITY;
+        bad |= !fin;
+        m = fin ? fmaxf(m, x) : m;
+      }
+    }
+    return m;
+  }
+  // the two parts of each value times inv (a power of two), at the swizzled places of row r of two K-major tiles
+  DLLM_DEV void split(float inv, int r, int quarter, uint8_t* hi_tile, uint8_t* lo_tile) const {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      uint32_t hi[4], lo[4];
+      float f[16];
+      bf16x8_to_f32(raw[2 * g], f);
+      bf16x8_to_f32(raw[2 * g + 1], f + 8);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t h2[2], l2[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float a = f[4 * i + 2 * j], b = f[4 * i + 2 * j + 1];
+          // an infinity becomes NaN (E4M3 has none), as the product with it would
+          a = fabsf(a) < INFINITY ? a * inv : __int_as_float(0x7fffffff);
+          b = fabsf(b) < INFINITY ? b * inv : __int_as_float(0x7fffffff);
+          h2[j] = kv8::f32x2_to_e4m3x2(a, b);
+          const uint32_t back = kv8::e4m3x2_to_f16x2(h2[j]);
+          const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&back));
+          l2[j] = kv8::f32x2_to_e4m3x2(a - hf.x, b - hf.y);
+        }
+        hi[i] = h2[0] | (h2[1] << 16);
+        lo[i] = l2[0] | (l2[1] << 16);
+      }
+      const int at = r * 128 + (((2 * quarter + g) ^ (r & 7)) << 4);
+      *reinterpret_cast<uint4*>(hi_tile + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(lo_tile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+  }
+};
+DLLM_DEV float max4(float m) {     // over the four threads of a row
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+// Address of a unit's query row (NULL past the last).
+DLLM_DEV const __nv_bfloat16* query_row(const Params& p, int b, int h, int rt, int r) {
+  const int R = rt * KT + r, qi = R / p.G;
+  return R < p.n_rows ? static_cast<const __nv_bfloat16*>(p.a.q) +
+                            (((int64_t)b * p.a.Lq + qi) * p.a.Hq + h * p.G + R - qi * p.G) * 128
+                      : nullptr;
+}
+// Q of a unit into shared memory by n threads (t = 0 .. n - 1, n a multiple of 128): parts and row scales.
+DLLM_DEV void stage_q(const Params& p, int b, int h, int rt, int t, int n, uint8_t* sQ, float* qscale,
+                      Quarter* pre /* the first pass's values, already loaded, or NULL */) {
+  for (int r = t >> 2; r < KT; r += n >> 2) {
+    Quarter q;
+    if (pre && r == t >> 2) {
+      q = *pre;
+    } else {
+      const __nv_bfloat16* src = query_row(p, b, h, rt, r);
+      q.load(src ? src + 32 * (t & 3) : nullptr);
+    }
+    bool bad;
+    const int k = kv8::scale_exp(max4(q.amax(bad)));
+    const unsigned any = __ballot_sync(0xffffffffu, bad) >> (threadIdx.x & 28) & 15u;
+    if ((t & 3) == 0) qscale[r] = any ? __int_as_float(0x7fffffff) : kv8::exp2i(k) * (p.a.scale * kLog2e);
+    q.split(kv8::exp2i(-k), r, t & 3, sQ, sQ + KSTAGE);
+  }
+}
+
+// This thread's 64 columns of S: the largest x = S c + lv over the visible ones (the first lim).
+template <bool MASK>
+DLLM_DEV float tile_max(const float* v, int lim, float rowc, const float4* run, int rstep) {
+  float mt = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const float4 rs = run[u * rstep];
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float x = v[16 * u + i];
+      if (!MASK || 16 * u + i < lim) m = fmaxf(m, x);
+    }
+    mt = fmaxf(mt, fmaf(m, rowc * rs.x, rs.y));
+  }
+  return mt;
+}
+// P of the 64 columns as f16 pairs; returns the sum of the weights with the V scales divided out.
+template <bool MASK>
+DLLM_DEV float tile_exp(const float* v, int lim, float rowc, const float4* run, int rstep, float shift, uint32_t* pk) {
+  float l = 0.f;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const float4 rs = run[u * rstep];
+    const float c = rowc * rs.x, d = rs.y + shift;
+    const uint64_t c2 = pk2(c, c), d2 = pk2(d, d);
+    uint64_t s2 = pk2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float x0, x1;
+      upk2(fma2(pk2(v[16 * u + 2 * i], v[16 * u + 2 * i + 1]), c2, d2), x0, x1);
+      float e0 = ex2(x0), e1 = ex2(x1);
+      if (MASK) {
+        if (16 * u + 2 * i >= lim) e0 = 0.f;
+        if (16 * u + 2 * i + 1 >= lim) e1 = 0.f;
+      }
+      pk[8 * u + i] = f16x2(e0, e1);
+      s2 = add2(s2, pk2(e0, e1));
+    }
+    float s0, s1;
+    upk2(s2, s0, s1);
+    l = fmaf(s0 + s1, rs.z, l);
+  }
+  return l;
+}
+// Barrier of the two warps that share 32 rows, with the OR of a predicate.
+DLLM_DEV bool pair_or(int id, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, %2, 64, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(id)
+      : "memory");
+  return r != 0;
+}
+DLLM_DEV void arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar)), "r"(n) : "memory");
+}
+
+__global__ void __launch_bounds__(NT, 1)
+attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = base;                          // hi, lo
+  uint8_t* sK = sQ + 2 * KSTAGE;               // [NK]
+  uint8_t* sW = sK + NK * KSTAGE;              // [NB] f16 V
+  uint8_t* sV = sW + NB * VTILE;               // [NV]
+  Bars& bar = *reinterpret_cast<Bars*>(sV + NV * KSTAGE);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Kv8AttnArgs& a = p.a;
+
+  if (tid == 0) {
+    bar.abort_flag = 0;
+    tc::mbar_init(&bar.q_full, 8);
+    tc::mbar_init(&bar.q_empty, 1 + 8);
+    for (int i = 0; i < NK; ++i) {
+      tc::mbar_init(&bar.k_full[i], 1);
+      tc::mbar_init(&bar.k_empty[i], 1);
+      tc::mbar_init(&bar.k_grant[i], 1);
+    }
+    for (int i = 0; i < NV; ++i) {
+      tc::mbar_init(&bar.v_full[i], 1);
+      tc::mbar_init(&bar.v_empty[i], 4);
+    }
+    for (int i = 0; i < NB; ++i) {
+      tc::mbar_init(&bar.w_full[i], 4);
+      tc::mbar_init(&bar.w_empty[i], 1);
+      tc::mbar_init(&bar.s_full[i], 1);
+      tc::mbar_init(&bar.p_ready[i], 8);
+    }
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&bar.r_full[i], 1);
+      tc::mbar_init(&bar.r_empty[i], 8);
+    }
+    tc::mbar_init(&bar.o_free, 8);
+    tc::mbar_init(&bar.done, 1);
+    tc::fence_mbar_init();
+    tc::prefetch_tmap(&tm_k);
+  }
+  if (warp == 1) tc::tmem_alloc(&bar.tmem_base, 512);
+  pdl_trigger();
+  if (warp == 0) {
+    pdl_wait();        // the lengths may come from the kernel before
+    const int64_t T = total_tiles(p);
+    const int64_t x0 = blockIdx.x * T / p.n_cta, x1 = (blockIdx.x + 1) * T / p.n_cta;
+    int b = 0, h = 0, rt = 0, ta = 0;
+    if (x1 > x0) locate(p, x0, b, h, rt, ta);
+    if (lane == 0) {
+      bar.walk[0] = b; bar.walk[1] = h; bar.walk[2] = rt; bar.walk[3] = ta; bar.walk[4] = (int)(x1 - x0);
+      bar.walk[5] = (int)T;
+    }
+  }
+  __syncthreads();
+  pdl_wait();
+  volatile int* abort_flag = &bar.abort_flag;
+  const uint32_t tS = bar.tmem_base, tO = bar.tmem_base + NB * 128;
+  Walk w;
+  w.start(p, bar.walk);
+  auto arrive = [&](uint64_t* b) {       // once for the warp, after all its lanes
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(b);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA: codes of the prefix tiles
+    if (tc::elect_one()) {
+      const uint64_t pol = p.reuse ? tc::policy_evict_last() : tc::policy_evict_first();
+      uint32_t ks = 0, vs = 0;      // slots of the K and V rings so far
+      uint32_t kq = 0, vq = 0;      // one past the last slot that this thread filled (for the drain)
+      bool ok = true;
+      for (; w.n > 0 && ok; w.next(p)) {
+        const int64_t bh = (int64_t)w.b * a.Hkv + w.h;
+        for (int t = w.ta; t < w.end() && ok; ++t) {
+          if (t >= w.tp) {
+            // own rows: the converters write two K stages (V goes past the code ring). This thread alone waits for
+            // free stages, in order, and hands them over: waiting for one's own slots only would miss whole phases
+            for (int i = t < w.tp + cdiv128(w.own) ? 2 : 1; i > 0 && ok; --i, ++ks) {
+              ok = wait_bar(&bar.k_empty[ks % NK], ((ks / NK) & 1) ^ 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+              if (ok) tc::mbar_arrive(&bar.k_grant[ks % NK]);
+            }
+            continue;
+          }
+          const uint32_t k = ks % NK, v = vs % NV;
+          if (!wait_bar(&bar.k_empty[k], ((ks / NK) & 1) ^ 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER)) { ok = false; break; }
+          tc::mbar_arrive_expect_tx(&bar.k_full[k], KSTAGE);
+          // rows past the cache read as zeros, rows past the prefix are masked
+          asm volatile(
+              "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+              " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(tc::smem_u32(sK + k * KSTAGE)),
+              "l"(reinterpret_cast<uint64_t>(&tm_k)), "r"(0), "r"(t * KT), "r"((int)bh),
+              "r"(tc::smem_u32(&bar.k_full[k])), "l"(pol)
+              : "memory");
+          kq = ++ks;
+          if (!wait_bar(&bar.v_empty[v], ((vs / NV) & 1) ^ 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER)) { ok = false; break; }
+          const uint32_t bytes = (uint32_t)min(KT, w.len - t * KT) * 128u;
+          tc::mbar_arrive_expect_tx(&bar.v_full[v], bytes);
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::
+                  "r"(tc::smem_u32(sV + v * KSTAGE)),
+              "l"(a.v_codes + (bh * a.cap + (int64_t)t * KT) * 128), "r"(bytes), "r"(tc::smem_u32(&bar.v_full[v])), "l"(pol)
+              : "memory");
+          vq = ++vs;
+        }
+      }
+      if (!ok) {    // let this thread's own copies land before the CTA leaves
+        for (uint32_t i = kq > NK ? kq - NK : 0; i < kq; ++i) tc::mbar_wait(&bar.k_full[i % NK], (i / NK) & 1, 1u << 12);
+        for (uint32_t i = vq > NV ? vq - NV : 0; i < vq; ++i) tc::mbar_wait(&bar.v_full[i % NV], (i / NV) & 1, 1u << 12);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA
+    if (tc::elect_one()) {
+      const uint32_t id_s = (1u << 4) | ((KT >> 3) << 17) | ((KT >> 4) << 24);                // E4M3 x E4M3 -> f32
+      const uint32_t id_o = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((KT >> 4) << 24);  // f16 x f16, B MN-major
+      const uint64_t dQ = tc::sdesc_k128(tc::smem_u32(sQ)), dK = tc::sdesc_k128(tc::smem_u32(sK));
+      const uint64_t dW = sdesc_mn128(tc::smem_u32(sW), VCHUNK);      // addresses step by bytes >> 4
+      // the S products run up to NB tiles ahead of P V, with a walk of their own
+      Walk ws = w;
+      int ts = w.ta;               // next tile of ws
+      uint32_t k = 0, kph = 0, sb = 0, seg_s = 0;
+      bool q_ready = false, ok = true;
+      auto issue_s = [&]() -> bool {
+        if (!q_ready) {
+          if (!wait_bar(&bar.q_full, seg_s & 1, abort_flag, a.status, ST_TIMEOUT_MMA)) return false;
+          q_ready = true;
+        }
+        const bool own = ts >= ws.tp && ts < ws.tp + cdiv128(ws.own);
+        const uint32_t d = tS + sb * 128;
+        for (int part = 0; part < (own ? 2 : 1); ++part) {
+          if (!wait_bar(&bar.k_full[k], kph, abort_flag, a.status, ST_TIMEOUT_MMA)) return false;
+          tc::fence_after_sync();
+          const uint64_t dk = dK + k * (KSTAGE >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)      // hi, then lo
+            mma_f8(d, dQ + (kk >> 2) * (KSTAGE >> 4) + (kk & 3) * 2, dk + (kk & 3) * 2, id_s, part != 0 || kk != 0);
+          tc::mma_commit(&bar.k_empty[k]);
+          if (++k == NK) {
+            k = 0;
+            kph ^= 1;
+          }
+        }
+        tc::mma_commit(&bar.s_full[sb]);
+        sb = sb == NB - 1 ? 0 : sb + 1;
+        if (++ts == ws.end()) {
+          tc::mma_commit(&bar.q_empty);
+          ws.next(p);
+          ts = 0;
+          ++seg_s;
+          q_ready = false;
+        }
+        return true;
+      };
+      // up to NB products ahead, but no further than the unit after the one P V works on: the Q of the unit after that
+      // is staged only when the softmax warps have left this one
+      int ahead = 0;
+      auto fill = [&](uint32_t seg) {
+        for (; ok && ahead < NB && ws.n > 0 && seg_s <= seg + 1; ++ahead) ok = issue_s();
+      };
+      fill(0);
+      uint32_t g = 0, ph = 0, seg = 0;
+      for (; w.n > 0 && ok; w.next(p), ++seg) {
+        fill(seg);
+        if (seg > 0 && !wait_bar(&bar.o_free, (seg - 1) & 1, abort_flag, a.status, ST_TIMEOUT_MMA)) break;
+        const int n = w.end() - w.ta;
+        for (int j = 0; j < n; ++j) {
+          if (!wait_bar(&bar.w_full[g], ph, abort_flag, a.status, ST_TIMEOUT_MMA) ||
+              !wait_bar(&bar.p_ready[g], ph, abort_flag, a.status, ST_TIMEOUT_MMA)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          const uint64_t dw = dW + g * (VTILE >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma_bf16_tmem_a(tO, tS + g * 128 + kk * 8, dw + kk * (2048 >> 4), id_o, (j != 0 || kk != 0) ? 1u : 0u);
+          tc::mma_commit(&bar.w_empty[g]);
+          --ahead;
+          fill(seg);     // into the buffer of P, behind P V in the issue order
+          if (!ok) break;
+          if (++g == NB) {
+            g = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      tc::mma_commit(&bar.done);
+      tc::mbar_wait(&bar.done, 0, 1u << 20);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------ scales of the prefix tiles
+    // lanes 0-7 K, 8-15 V, one per 16 keys; the next of this warp's tiles is loaded while the last waits for its slot
+    const int64_t runs = (a.cap + a.S - 1) / a.S;
+    uint32_t pt = 0;
+    float held = 0.f;
+    bool have = false;
+    uint32_t held_pt = 0;
+    auto put = [&]() {
+      const uint32_t s = held_pt & 3;
+      wait_bar(&bar.r_empty[s], ((held_pt >> 2) & 1) ^ 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+      const float v = fmaxf(__shfl_down_sync(0xffffffffu, held, 8), 5.421010862427522e-20f);   // 2^-64
+      if (lane < 8) bar.run[s][lane] = make_float4(held, log2f(v), 1.0f / v, 0.f);
+      arrive(&bar.r_full[s]);
+    };
+    for (; w.n > 0; w.next(p)) {
+      const int64_t bh = (int64_t)w.b * a.Hkv + w.h;
+      const int t1 = min(w.end(), w.tp);
+      for (int t = w.ta; t < t1; ++t, ++pt) {
+        if ((int)(pt & 1) != warp - 2) continue;
+        float x = 0.f;      // 16 keys past the prefix: masked, any finite scale will do
+        const int key = t * KT + 16 * (lane & 7);
+        if (lane < 16 && key < w.len) x = (lane < 8 ? a.k_scale : a.v_scale)[bh * runs + key / a.S];
+        if (have) put();
+        held = x;
+        held_pt = pt;
+        have = true;
+      }
+    }
+    if (have) put();
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------------ converters
+    const int ct = tid - 384;
+    const uint32_t cw = warp - 12;
+    uint32_t k = 0, v = 0, vph = 0, g = 0, wph = 1, seg = 0, granted = 0;
+    for (; w.n > 0; w.next(p), ++seg) {
+      const int64_t bh = (int64_t)w.b * a.Hkv + w.h;
+      if (seg > 0) {   // the first unit's Q is staged by the softmax warps, which have nothing to do yet
+        Quarter pre;
+        const __nv_bfloat16* src = query_row(p, w.b, w.h, w.rt, ct >> 2);
+        pre.load(src ? src + 32 * (ct & 3) : nullptr);
+        wait_bar(&bar.q_empty, (seg - 1) & 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+        stage_q(p, w.b, w.h, w.rt, ct, 128, sQ, bar.qscale, &pre);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_n(&bar.q_full, 2);
+      }
+      for (int t = w.ta; t < w.end(); ++t) {
+        uint8_t* dst = sW + g * VTILE;
+        wait_bar(&bar.w_empty[g], wph, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+        if (t < w.tp) {
+          const int n = min(KT, w.len - t * KT);
+          wait_bar(&bar.v_full[v], vph, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+          const uint8_t* src = sV + v * KSTAGE;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int id = i * 128 + ct, key = id >> 3, e = id & 7;      // 16 codes: key, columns 16 e ..
+            uint4 u = *reinterpret_cast<const uint4*>(src + id * 16);
+            if (key >= n) u = make_uint4(0, 0, 0, 0);    // not loaded: weight 0 times anything but NaN
+            uint32_t h[8];
+            kv8::e4m3x4_to_f16x4(u.x, h[0], h[1]);
+            kv8::e4m3x4_to_f16x4(u.y, h[2], h[3]);
+            kv8::e4m3x4_to_f16x4(u.z, h[4], h[5]);
+            kv8::e4m3x4_to_f16x4(u.w, h[6], h[7]);
+            // granules 2 (e & 3) and the next of chunk e >> 2; the upper half-group writes them in the other order, so
+            // that the eight lanes of a key touch eight different 16-byte columns
+            uint8_t* row = dst + (e >> 2) * VCHUNK + key * 128;
+            const int g0 = (e & 3) * 2, sw = e >> 2;
+            const uint4 x0 = make_uint4(h[0], h[1], h[2], h[3]), x1 = make_uint4(h[4], h[5], h[6], h[7]);
+            *reinterpret_cast<uint4*>(row + (((g0 + sw) ^ (key & 7)) << 4)) = sw ? x1 : x0;
+            *reinterpret_cast<uint4*>(row + (((g0 + 1 - sw) ^ (key & 7)) << 4)) = sw ? x0 : x1;
+          }
+          arrive(&bar.v_empty[v]);
+          if (++v == NV) {
+            v = 0;
+            vph ^= 1;
+          }
+          k = k == NK - 1 ? 0 : k + 1;
+        } else {
+          // own rows (none at all in a unit without keys): four threads per key, 32 keys at a time
+          const int j0 = (t - w.tp) * KT, n = min(KT, w.own - j0), parts = n > 0 ? 2 : 1;
+          const int64_t at = (bh * a.cap_own + j0) * 128 + 32 * (ct & 3);
+          float mk = 0.f, mv = 0.f;
+          for (int r = ct >> 2; r < n; r += 32) {
+            Quarter q;
+            bool bad;
+            q.load(static_cast<const __nv_bfloat16*>(a.k_own) + at + r * 128);
+            mk = fmaxf(mk, q.amax(bad));
+            q.load(static_cast<const __nv_bfloat16*>(a.v_own) + at + r * 128);
+            mv = fmaxf(mv, q.amax(bad));
+          }
+          mk = warp_max(mk);
+          mv = warp_max(mv);
+          if (lane == 0) {
+            bar.red[0][cw] = mk;
+            bar.red[1][cw] = mv;
+          }
+          tc::named_bar_sync(kBarConv, 128);
+          const int ek = kv8::scale_exp(fmaxf(fmaxf(bar.red[0][0], bar.red[0][1]), fmaxf(bar.red[0][2], bar.red[0][3])));
+          const int ev = kv8::scale_exp(fmaxf(fmaxf(bar.red[1][0], bar.red[1][1]), fmaxf(bar.red[1][2], bar.red[1][3])));
+          if (ct == 0) bar.run_own[g] = make_float4(kv8::exp2i(ek), (float)ev, kv8::exp2i(-ev), 0.f);
+          const uint32_t k0 = k, k1 = parts == 2 ? (k + 1) % NK : k;
+          for (int i = 0; i < parts; ++i) {
+            const uint32_t kk = i ? k1 : k0;
+            wait_bar(&bar.k_grant[kk], (granted >> kk) & 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+            granted ^= 1u << kk;
+          }
+          const float ik = kv8::exp2i(-ek), iv = kv8::exp2i(-ev);
+          for (int r = ct >> 2; r < KT; r += 32) {
+            Quarter q;
+            q.load(r < n ? static_cast<const __nv_bfloat16*>(a.k_own) + at + r * 128 : nullptr);
+            q.split(ik, r, ct & 3, sK + k0 * KSTAGE, sK + k1 * KSTAGE);
+            q.load(r < n ? static_cast<const __nv_bfloat16*>(a.v_own) + at + r * 128 : nullptr);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float f[8];
+              bf16x8_to_f32(q.raw[i], f);
+              const int gr = 4 * (ct & 3) + i;      // granule of 8 values: chunk gr >> 3
+              *reinterpret_cast<uint4*>(dst + (gr >> 3) * VCHUNK + r * 128 + (((gr & 7) ^ (r & 7)) << 4)) =
+                  make_uint4(f16x2(f[0] * iv, f[1] * iv), f16x2(f[2] * iv, f[3] * iv), f16x2(f[4] * iv, f[5] * iv),
+                             f16x2(f[6] * iv, f[7] * iv));
+            }
+          }
+          fence_async_smem();
+          tc::named_bar_sync(kBarConv, 128);
+          if (ct < parts) tc::mbar_arrive(&bar.k_full[ct ? k1 : k0]);
+          k = (k + parts) % NK;
+        }
+        fence_async_smem();
+        arrive(&bar.w_full[g]);
+        if (++g == NB) {
+          g = 0;
+          wph ^= 1;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, pair = kBarPair + (warp & 3);
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    uint32_t it = 0, g = 0, ph = 0, pt = 0, seg = 0;
+    if (w.n > 0) {
+      stage_q(p, w.b, w.h, w.rt, tid - 128, 256, sQ, bar.qscale, nullptr);
+      fence_async_smem();
+      arrive(&bar.q_full);
+    }
+    for (; w.n > 0; w.next(p), ++seg) {
+      const int R = w.rt * KT + row;
+      const bool live = R < p.n_rows, warp_live = w.rt * KT + (warp & 3) * 32 < p.n_rows;
+      const int qi = (live ? R : p.n_rows - 1) / p.G;
+      const int own_lim = a.k_own ? (int)min((int64_t)a.Lq, ((int64_t)(qi / a.blk_len) + 1) * a.blk_len) : 0;
+      wait_bar(&bar.q_full, seg & 1, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+      const float rowc = bar.qscale[row];
+      arrive(&bar.q_empty);
+      float mg = -INFINITY, l = 0.f;
+      for (int t = w.ta; t < w.end(); ++t, ++it) {
+        const bool pre = t < w.tp;
+        const uint32_t rs = pt & 3;
+        const int lim = (pre ? w.len - t * KT : own_lim - (t - w.tp) * KT) - 64 * half;
+        if (pre)
+          wait_bar(&bar.r_full[rs], (pt >> 2) & 1, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+        else
+          wait_bar(&bar.w_full[g], ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+        wait_bar(&bar.s_full[g], ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+        if (warp_live) {
+          const float4* run = pre ? &bar.run[rs][4 * half] : &bar.run_own[g];
+          const int rstep = pre ? 1 : 0;
+          const bool fast = __all_sync(0xffffffffu, lim >= 64);
+          tc::fence_after_sync();
+          const uint32_t tSg = tS + g * 128 + lane_off;
+          float v[64];
+          tmem_ld64(tSg + 64 * half, v);
+          const float mt = fast ? tile_max<false>(v, lim, rowc, run, rstep) : tile_max<true>(v, lim, rowc, run, rstep);
+          // also orders the other warp's loads of S before this one's P, which overwrites them
+          if (pair_or(pair, mt > mg + kRescale)) {
+            bar.xm[it & 1][half][row] = mt;
+            tc::named_bar_sync(pair, 64);
+            const float mm = fmaxf(bar.xm[it & 1][0][row], bar.xm[it & 1][1][row]);
+            float alpha = 1.f;
+            if (mm > mg + kRescale) {
+              alpha = mg == -INFINITY ? 1.f : ex2(mg - mm);
+              mg = mm;
+            }
+            l *= alpha;
+            if (t > w.ta && __any_sync(0xffffffffu, alpha != 1.f)) {
+              // O holds the unit's previous tiles once the last P V completes. S of this tile is complete, so the P V
+              // three tiles ago, issued before it, is too: the last one's barrier is at most one phase behind.
+              wait_bar(&bar.w_empty[g == 0 ? NB - 1 : g - 1], g == 0 ? ph ^ 1 : ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+              __syncwarp();
+              tc::fence_after_sync();
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float x[32];
+                const uint32_t at = tO + 64 * half + 32 * c + lane_off;
+                tmem_ld32(at, x);
+                uint32_t r32[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r32[i] = __float_as_uint(x[i] * alpha);
+                tc::tmem_st32(at, r32);
+              }
+            }
+          }
+          const float shift = kOff - (mg == -INFINITY ? 0.f : mg);
+          uint32_t pk[32];
+          l += fast ? tile_exp<false>(v, lim, rowc, run, rstep, shift, pk) : tile_exp<true>(v, lim, rowc, run, rstep, shift, pk);
+          tc::tmem_st32(tSg + 32 * half, pk);
+          tc::tmem_st_wait();
+          tc::fence_before_sync();
+        }
+        arrive(&bar.p_ready[g]);
+        if (pre) {
+          if (lane == 0) tc::mbar_arrive(&bar.r_empty[rs]);
+          ++pt;
+        }
+        if (++g == NB) {
+          g = 0;
+          ph ^= 1;
+        }
+      }
+      // the unit's last P V
+      wait_bar(&bar.w_empty[g == 0 ? NB - 1 : g - 1], g == 0 ? ph ^ 1 : ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+      const bool whole = w.ta == 0 && w.end() == w.tiles;
+      if (warp_live) {
+        bar.xl[seg & 1][half][row] = l;
+        tc::named_bar_sync(pair, 64);
+        const float L = bar.xl[seg & 1][0][row] + bar.xl[seg & 1][1][row];
+        const float inv = L == 0.f ? 0.f : 1.0f / L;
+        const bool put = !*abort_flag && live;
+        const int64_t qh = ((int64_t)w.b * a.Lq + qi) * a.Hq + w.h * p.G + (live ? R - qi * p.G : 0);
+        float4* part = reinterpret_cast<float4*>(p.part + ((int64_t)blockIdx.x * 2 + (w.ta == 0 ? 1 : 0)) * kPart);
+        __syncwarp();
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = 64 * half + 32 * c;
+          float o[32];
+          tmem_ld32(tO + col + lane_off, o);
+          if (put && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + qh * 128 + col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t u[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                __nv_bfloat162 r = __floats2bfloat162_rn(o[8 * i + 2 * j] * inv, o[8 * i + 2 * j + 1] * inv);
+                u[j] = *reinterpret_cast<uint32_t*>(&r);
+              }
+              dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          } else if (put) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              part[(col / 4 + i) * KT + row] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+          __syncwarp();
+        }
+        tc::fence_before_sync();
+        if (put && half == 0) {
+          if (!whole) part[32 * KT + row] = make_float4(mg, L, 0.f, 0.f);
+          else if (a.lse_out) a.lse_out[qh] = L == 0.f ? -INFINITY : (mg - kOff + log2f(L)) * kLn2;
+        }
+      }
+      if (tid == 128 && w.ta == 0) {
+        // for the join: CTA c owns tiles [c T / n, (c + 1) T / n), so tile x is in c = ((x + 1) n - 1) / T
+        const int64_t T = bar.walk[5], s = (blockIdx.x + 1) * T / p.n_cta - w.n, e = s + w.tiles;
+        const int c1 = (int)((e * p.n_cta - 1) / T), share = T < p.n_cta ? w.tiles : c1 - (int)blockIdx.x + 1;
+        p.span[((int64_t)w.b * a.Hkv + w.h) * p.n_rt + w.rt] = make_int4((int)s, whole ? 0 : share, (int)T, 0);
+      }
+      arrive(&bar.o_free);
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(bar.tmem_base, 512);
+  }
+}
+
+// Joins the partial results of the units that span several CTAs: one block per unit and 16 output columns, one thread
+// per row, the CTAs in order.
+constexpr int kMergeCols = 16;
+__global__ void __launch_bounds__(KT) attn_kv8_merge_kernel(const __grid_constant__ Params p) {
+  pdl_enter();
+  const Kv8AttnArgs& a = p.a;
+  const int row = threadIdx.x, part_col = blockIdx.x % (128 / kMergeCols);
+  const int64_t unit = blockIdx.x / (128 / kMergeCols);
+  const int4 sp = p.span[unit];
+  const int rt = (int)(unit % p.n_rt), R = rt * KT + row;
+  if (sp.y == 0 || R >= p.n_rows) return;
+  const int64_t T = sp.z;
+  const int c0 = (int)(((int64_t)(sp.x + 1) * p.n_cta - 1) / T);
+  // the k-th CTA of the unit; with more CTAs than tiles some own none, and every tile has a CTA of its own
+  auto slot = [&](int k) {
+    const int c = T < p.n_cta ? (int)(((int64_t)(sp.x + k + 1) * p.n_cta - 1) / T) : c0 + k;
+    return reinterpret_cast<const float4*>(p.part) + ((int64_t)c * 2 + (k == 0 ? 1 : 0)) * (kPart / 4);
+  };
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int k = 0; k < sp.y; ++k) M = fmaxf(M, slot(k)[32 * KT + row].x);
+  float L = 0.f, o[kMergeCols];
+#pragma unroll
+  for (int i = 0; i < kMergeCols; ++i) o[i] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < sp.y; ++k) {
+    const float4* s = slot(k);
+    const float4 ml = s[32 * KT + row];
+    const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+    L = fmaf(wt, ml.y, L);
+#pragma unroll
+    for (int i = 0; i < kMergeCols / 4; ++i) {
+      const float4 x = s[(part_col * (kMergeCols / 4) + i) * KT + row];
+      o[4 * i] = fmaf(wt, x.x, o[4 * i]);
+      o[4 * i + 1] = fmaf(wt, x.y, o[4 * i + 1]);
+      o[4 * i + 2] = fmaf(wt, x.z, o[4 * i + 2]);
+      o[4 * i + 3] = fmaf(wt, x.w, o[4 * i + 3]);
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.0f / L;
+  const int64_t bh = unit / p.n_rt;
+  const int b = (int)(bh / a.Hkv), h = (int)(bh - (int64_t)b * a.Hkv), qi = R / p.G;
+  const int64_t qh = ((int64_t)b * a.Lq + qi) * a.Hq + h * p.G + R - qi * p.G;
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + qh * 128 + part_col * kMergeCols);
+#pragma unroll
+  for (int i = 0; i < kMergeCols / 8; ++i) {
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      __nv_bfloat162 r = __floats2bfloat162_rn(o[8 * i + 2 * j] * inv, o[8 * i + 2 * j + 1] * inv);
+      u[j] = *reinterpret_cast<uint32_t*>(&r);
+    }
+    dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  if (part_col == 0 && a.lse_out) a.lse_out[qh] = L == 0.f ? -INFINITY : (M - kOff + log2f(L)) * kLn2;
+}
+
+int encode_codes(CUtensorMap* m, const void* codes, int64_t cap, int64_t bh) {
+  EncodeTiledFn enc = encoder();
+  if (!enc) {
+    dllm_host::set_error("cuTensorMapEncodeTiled unavailable");
+    return DLLM_ERR_CUDA;
+  }
+  const cuuint64_t dims[3] = {128, (cuuint64_t)cap, (cuuint64_t)bh};
+  const cuuint64_t str[2] = {128, (cuuint64_t)cap * 128};
+  const cuuint32_t box[3] = {128, KT, 1}, es[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, str, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    dllm_host::set_error("attention over 8-bit codes: cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return DLLM_ERR_CUDA;
+  }
+  return DLLM_OK;
+}
+
+// Own key tiles of all row tiles (own_keys on the host).
+int64_t own_tiles_sum(const Kv8AttnArgs& a, int n_rt, int G) {
+  if (!a.k_own) return 0;
+  int64_t t = 0;
+  for (int rt = 0; rt < n_rt; ++rt) {
+    const int last_q = (std::min((int64_t)(rt + 1) * KT, (int64_t)a.Lq * G) - 1) / G;
+    t += (std::min<int64_t>(a.Lq, ((int64_t)(last_q / a.blk_len) + 1) * a.blk_len) + KT - 1) / KT;
+  }
+  return t;
+}
+
+}  // namespace
+
+// Partial results of every CTA, then the units' spans.
+size_t attn_kv8_tc_workspace_bytes(int B, int Lq, int Hq, int Hkv) {
+  const size_t units = (size_t)B * Hkv * (((size_t)Lq * (Hq / Hkv) + KT - 1) / KT);
+  return (size_t)num_sms() * 2 * kPart * sizeof(float) + units * sizeof(int4);
+}
+
+int launch_attn_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
+  Params p;
+  p.a = a;
+  p.G = a.Hq / a.Hkv;
+  p.n_rows = a.Lq * p.G;
+  p.n_rt = (p.n_rows + KT - 1) / KT;
+  p.own_sum = own_tiles_sum(a, p.n_rt, p.G);
+  p.part = static_cast<float*>(a.ws);
+  p.span = reinterpret_cast<int4*>(p.part + (size_t)num_sms() * 2 * kPart);
+  p.reuse = p.n_rt > 1;
+  // most tiles there can be (lengths may be shorter): no more CTAs than those
+  const int64_t tp = (a.P + KT - 1) / KT;
+  const int64_t most = (int64_t)a.B * a.Hkv * (p.n_rt * (a.k_own ? tp : std::max<int64_t>(tp, 1)) + p.own_sum);
+  DLLM_REQUIRE(most < (1ll << 31), DLLM_ERR_UNSUPPORTED, "block_attn_kv8: too many rows and keys for one call");
+  p.n_cta = (int)std::min<int64_t>(num_sms(), most);
+  CUtensorMap mk;
+  // without prefix rows no tile is loaded; the map then describes the queries' memory, which exists
+  int st = a.P > 0 ? encode_codes(&mk, a.k_codes, a.cap, (int64_t)a.B * a.Hkv) : encode_codes(&mk, a.q, 1, 1);
+  if (st) return st;
+  st = set_max_smem<attn_kv8_tc_kernel>(SMEM);
+  if (st) return st;
+  launch_pdl(attn_kv8_tc_kernel, p.n_cta, NT, SMEM, s, mk, p);
+  DLLM_CHECK_LAUNCH("attn_kv8_tc_kernel");
+  if (p.n_cta > 1) {
+    launch_pdl(attn_kv8_merge_kernel, (unsigned)((int64_t)a.B * a.Hkv * p.n_rt * (128 / kMergeCols)), KT, 0, s, p);
+    DLLM_CHECK_LAUNCH("attn_kv8_merge_kernel");
+  }
+  return DLLM_OK;
+}
+
+}  // namespace dllm

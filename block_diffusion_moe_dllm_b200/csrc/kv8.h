@@ -3,8 +3,23 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stddef.h>
+#include <atomic>
+#include "common.cuh"
 
 namespace dllm {
+
+// Raises a kernel's dynamic shared memory limit on the current device (once per device and kernel).
+template <auto kernel>
+inline int set_max_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};      // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return DLLM_OK;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return dllm_host::cuda_status(e, "cudaFuncSetAttribute");
+  if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+  return DLLM_OK;
+}
 
 struct Kv8StoreArgs {
   int B, Hkv, d, n, cap_src, src_row, cap, dst_row, S, dtype, pos_stride;
@@ -43,6 +58,9 @@ struct Kv8AttnArgs {
 size_t attn_kv8_workspace_bytes(int B, int Lq, int Hq, int Hkv, int d, int P, int own, int dtype);
 int launch_attn_kv8(const Kv8AttnArgs& a, cudaStream_t s);
 int launch_attn_mass_kv8(const Kv8AttnArgs& a, cudaStream_t s);
+// tensor-core variants (bf16)
+size_t attn_kv8_tc_workspace_bytes(int B, int Lq, int Hq, int Hkv);
+int launch_attn_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s);
 // SIMT variants (any storage type)
 size_t attn_kv8_simt_workspace_bytes(int B, int Lq, int Hq, int Hkv, int d, int P, int own);
 int launch_attn_kv8_simt(const Kv8AttnArgs& a, cudaStream_t s);

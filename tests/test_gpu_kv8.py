@@ -185,6 +185,9 @@ ATTN = [
     ("bf16", 1, 200, 4, 1, 128, 384, 128, 32, (383,), True), ("bf16", 1, 131, 3, 3, 128, 0, 16, 1, None, True),
     ("bf16", 2, 16, 48, 2, 128, 140, 32, 16, (140, 13), False), ("bf16", 1, 300, 16, 2, 128, 70, 16, 4096, None, True),
     ("bf16", 9, 4, 4, 2, 128, 1100, 64, 4, (1100, 3, 0, 640, 1024, 1, 128, 129, 900), True),
+    ("bf16", 8, 260, 16, 4, 128, 200, 32, 32, (200, 0, 129, 128, 1, 77, 200, 3), True),    # many units a CTA, several
+    ("bf16", 300, 1, 4, 4, 128, 0, 16, 1, None, True),                                    # own tiles in a row
+    ("bf16", 200, 1, 8, 4, 128, 130, 16, 1, tuple(i % 3 * 65 for i in range(200)), False),
     ("bf16", 1, 2, 16, 1, 128, 9000, 128, 1, (8999,), True), ("bf16", 40, 1, 1, 1, 128, 50, 16, 1, tuple(range(40)), True)]
 
 
