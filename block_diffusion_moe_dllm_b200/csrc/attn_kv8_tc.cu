@@ -411,6 +411,11 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     if (lane == 0) tc::mbar_arrive(b);
   };
 
+  // The four warpgroups launch with 128 registers a thread each and go to 104, 152, 152, 104 (the same sum): a softmax
+  // thread holds 64 scores beside what the rare rescale of O needs. Nothing may spill: shared memory leaves the L1 next to
+  // nothing, so local memory is L2 (a build with 424 bytes of spills took 3 times as long).
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA: codes of the prefix tiles
     if (tc::elect_one()) {
@@ -536,7 +541,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       tc::mma_commit(&bar.done);
       tc::mbar_wait(&bar.done, 0, 1u << 20);
     }
-  } else if (warp < 4) {
+  } else {
     // ------------------------------------------------------------------ scales of the prefix tiles
     // lanes 0-7 K, 8-15 V, one per 16 keys; the next of this warp's tiles is loaded while the last waits for its slot
     const int64_t runs = (a.cap + a.S - 1) / a.S;
@@ -566,8 +571,10 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       }
     }
     if (have) put();
+  }
   } else if (warp >= 12) {
     // ------------------------------------------------------------------ converters
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     const int ct = tid - 384;
     const uint32_t cw = warp - 12;
     uint32_t k = 0, v = 0, vph = 0, g = 0, wph = 1, seg = 0, granted = 0;
@@ -674,6 +681,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     }
   } else {
     // ------------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, pair = kBarPair + (warp & 3);
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t it = 0, g = 0, ph = 0, pt = 0, seg = 0;
@@ -726,15 +734,21 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
               wait_bar(&bar.w_empty[g == 0 ? NB - 1 : g - 1], g == 0 ? ph ^ 1 : ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
               __syncwarp();
               tc::fence_after_sync();
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {      // 8 columns at a time: the scores stay in registers meanwhile
+                const uint32_t at = tO + 64 * half + 8 * c + lane_off;
+                uint32_t x[8];
+                asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+                             "tcgen05.wait::ld.sync.aligned;"
+                             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
+                               "=r"(x[7])
+                             : "r"(at)
+                             : "memory");
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                float x[32];
-                const uint32_t at = tO + 64 * half + 32 * c + lane_off;
-                tmem_ld32(at, x);
-                uint32_t r32[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) r32[i] = __float_as_uint(x[i] * alpha);
-                tc::tmem_st32(at, r32);
+                for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
+                asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
+                             "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                             : "memory");
               }
             }
           }
