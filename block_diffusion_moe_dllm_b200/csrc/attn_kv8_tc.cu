@@ -16,20 +16,23 @@
 //               four products).
 //   softmax     one thread per row; x = S * (2^k scale log2(e) k_scale) + log2(v_scale) - m: the V scale of each run rides
 //               in the exponent, so that P V needs no scaled copy of V; the row sum divides it out again run by run.
-//               P = 2^(x + 6) as f16, with m within 2^8 of the true maximum: the largest weight is in [2^-2, 2^14] and a
-//               weight keeps 11 bits down to 2^-20 of it and is dropped below 2^-31.
+//               P = 2^(x + 2) as f16, with m within 2^13 of the largest score so far: the largest weight is in [2^2, 2^15],
+//               a weight keeps 11 bits down to 2^-16 of it and is dropped below 2^-27 (n keys lose at most n 2^-27 of the
+//               largest weight). A move of m waits for the tensor pipe and costs about 5000 clocks; at 2^8 a third of the
+//               tiles of normal scores moved it for some row.
 //   O += P V    kind::f16 with A = P from TMEM and B = V as f16 (every E4M3 value is one), written from the codes by four
 //               converter warps into the MN-major layout.
 // Tensor time of a tile: 8 + 8 MMAs of 64 clocks, and about 250 clocks for each of the two changes of the instruction
 // descriptor (measured on bare loops: 512 clocks per 8 MMAs of one kind, 756 when S and P V alternate, whatever their
 // operand sources), so about 1510 clocks, against 1420 for the tile's bytes at one SM's share of the HBM rate and 1024
 // for its exponentials. Three S buffers and one O in TMEM keep three tiles in flight, so that the tensor pipe does not
-// wait for a softmax; two threads share a row (columns [0, 64) and [64, 128) of every tile), whose common reference
-// maximum moves only when a tile exceeds it by 2^8: a vote of the row's two warps decides, and only then do they exchange
-// maxima and rescale O.
+// wait for a softmax. Two softmax groups of four warps take alternate tiles, one thread per row, so that the exponentials
+// of one overlap the loads, maxima and barriers of the other (two threads per row on the same tile took 2700 clocks a
+// tile, 1500 of them exponentials). The row's reference maximum is common to both: a group passes it on to the other's
+// next tile as soon as it knows its own tile's maximum, and moves it (rescaling O) only when that exceeds it by 2^13.
 //
-// Roles: warp 0 TMA, warp 1 MMA, warps 2 and 3 the runs' scales (alternate prefix tiles), warps 4-7 and 8-11 softmax (lower
-// and upper half of the columns), warps 12-15 convert Q, V and the own rows. Warps whose rows are all past the last only
+// Roles: warp 0 TMA, warp 1 MMA, warps 2 and 3 the runs' scales (alternate prefix tiles), warps 4-7 and 8-11 softmax (even
+// and odd tiles), warps 12-15 convert Q, V and the own rows. Warps whose rows are all past the last only
 // keep count. Every wait is bounded; a wait that gives up sets the abort flag and the status word, after which every
 // role runs through its loops without waiting, issuing or storing anything.
 #include "attn_tc.cuh"
@@ -47,10 +50,12 @@ constexpr int KSTAGE = 128 * 128;          // K or V codes of a tile: 16 KB
 constexpr int VTILE = 2 * 128 * 64 * 2;    // V of a tile as f16: two 64-wide chunks of 16 KB
 constexpr int VCHUNK = VTILE / 2;
 constexpr int NK = 3, NV = 2, NB = 3;      // stages of the K and V code rings; S and f16 V buffers
-constexpr float kRescale = 8.f;            // the reference maximum moves when a tile exceeds it by 2^8
-constexpr float kOff = 6.f;                // P is 2^6 times the weight relative to the reference maximum
+constexpr float kRescale = 13.f;           // the reference maximum moves when a tile exceeds it by 2^13
+constexpr float kOff = 2.f;                // P is 2^2 times the weight relative to the reference maximum
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kBarConv = 1, kBarPair = 2;  // named barriers: the 128 converter threads; 2 + i: the two warps of rows 32 i ..
+// named barriers: the 128 converter threads; then three for the two warps of rows 32 i ..: a reference maximum from group 0
+// to group 1, from group 1 to group 0, and both at the end of a unit
+constexpr int kBarConv = 1, kBarPair = 2;
 constexpr int kPart = 33 * 128 * 4;        // floats of one partial result: 32 float4 columns and (m, l, -, -), by row
 
 struct Bars {
@@ -59,18 +64,19 @@ struct Bars {
   uint64_t k_grant[NK];                    // a free K stage handed to the converters, for own rows
   uint64_t v_full[NV], v_empty[NV];
   uint64_t w_full[NB], w_empty[NB];        // f16 V of a tile; empty = the tile's P V is complete
-  uint64_t s_full[NB], p_ready[NB];
+  uint64_t s_full[2 * NB], p_ready[NB];    // S of tile i: barrier i mod 6, so that one group alone waits for each
   uint64_t r_full[4], r_empty[4];          // scales of a prefix tile
   uint64_t o_free;                         // O of the finished unit has been read
   uint64_t done;
   uint32_t tmem_base;
   int abort_flag;
-  int walk[6];                             // b, h, rt, first tile, number of tiles of this CTA; tiles of all CTAs
-  float red[2][4];                         // own rows' largest magnitudes, by converter warp
+  int walk[7];                             // b, h, rt, first tile, number of tiles of this CTA, prefix length of b; all tiles
+  uint32_t red[2][4];                      // own rows' largest magnitudes (bf16 bits), by converter warp
   float qscale[KT];                        // per row: 2^k * scale * log2(e)
   float4 run[4][8];                        // per prefix tile and 16 keys: k scale, log2(v scale), 1 / v scale
   float4 run_own[NB];                      // of an own tile
-  float xm[2][2][KT], xl[2][2][KT];        // [parity][column half][row]: maxima, sums
+  float ref[2][KT];                        // [tile parity][row]: reference maximum passed on
+  float2 ml[2][2][KT];                     // [unit parity][group][row]: reference maximum and sum
 };
 constexpr int SMEM = 1024 + 2 * KSTAGE /*Q*/ + NK * KSTAGE + NV * KSTAGE + NB * VTILE + (int)sizeof(Bars);
 static_assert(SMEM <= 232448, "shared memory budget");
@@ -82,7 +88,7 @@ struct Params {
   int64_t own_sum;            // own key tiles of all row tiles of a (b, kv head)
   int n_cta;
   float* part;                // [n_cta][2][kPart]
-  int4* span;                 // [units]: first tile, CTAs that share the unit (0: one, already written), all tiles
+  int2* span;                 // [units]: first and last CTA that work on the unit (one alone has written its rows)
   int reuse;                  // several row tiles read the same keys: keep them in L2
 };
 
@@ -93,94 +99,100 @@ DLLM_DEV int own_keys(const Params& p, int rt) {
   return (int)min((int64_t)p.a.Lq, ((int64_t)(last_q / p.a.blk_len) + 1) * p.a.blk_len);
 }
 DLLM_DEV int cdiv128(int x) { return (int)(((unsigned)x + 127u) >> 7); }
-// Key tiles of all units of batch row b: at least one per unit, so that rows without keys are written too.
-DLLM_DEV int64_t row_tiles(const Params& p, int b) {
+// Key tiles of all units of batch row b: at least one per unit, so that rows without keys are written too. The host
+// checks that all of them stay below 2^31.
+DLLM_DEV uint32_t row_tiles(const Params& p, int b) {
   const int tp = cdiv128(kv8::prefix_len(p.a.lens, b, p.a.P));
-  return (int64_t)p.a.Hkv * ((int64_t)p.n_rt * (p.a.k_own ? tp : max(tp, 1)) + p.own_sum);
+  return (uint32_t)p.a.Hkv * ((uint32_t)p.n_rt * (uint32_t)(p.a.k_own ? tp : max(tp, 1)) + (uint32_t)p.own_sum);
 }
+
+// CTA c's share of T tiles: the first T mod n CTAs take one more than the others.
+struct Share {
+  uint32_t q, r;
+  DLLM_DEV Share(uint32_t T, uint32_t n) : q(T / n), r(T - T / n * n) {}
+  DLLM_DEV uint32_t first(uint32_t c) const { return c * q + min(c, r); }
+  DLLM_DEV uint32_t cta_of(uint32_t x) const {
+    const uint32_t big = r * (q + 1);
+    return x < big ? x / (q + 1) : r + (x - big) / max(q, 1u);
+  }
+};
 
 // Position in the sequence of key tiles, advanced unit by unit; every role walks it by itself.
 struct Walk {
   int b, h, rt, ta, n;      // unit, first tile in it, tiles left to this CTA
   int len, tp, own, tiles;  // of the unit: prefix length, prefix tiles, own keys, all tiles
-  DLLM_DEV void unit(const Params& p, bool new_row) {
-    if (new_row) {
-      len = kv8::prefix_len(p.a.lens, b, p.a.P);
-      tp = cdiv128(len);
-    }
+  DLLM_DEV void unit(const Params& p) {
     own = own_keys(p, rt);
     tiles = max(1, tp + cdiv128(own));
   }
   DLLM_DEV void start(const Params& p, const int* w) {
-    b = w[0]; h = w[1]; rt = w[2]; ta = w[3]; n = w[4];
-    if (n > 0) unit(p, true);
+    b = w[0]; h = w[1]; rt = w[2]; ta = w[3]; n = w[4]; len = w[5];
+    tp = cdiv128(len);
+    if (n > 0) unit(p);
   }
   DLLM_DEV int end() const { return min(tiles, ta + n); }    // the CTA's tiles of this unit: [ta, end())
   DLLM_DEV void next(const Params& p) {
     n -= end() - ta;
     ta = 0;
-    bool row = false;
     if (++rt == p.n_rt) {
       rt = 0;
       if (++h == p.a.Hkv) {
         h = 0;
         ++b;
-        row = true;
+        if (n > 0) {
+          len = kv8::prefix_len(p.a.lens, b, p.a.P);
+          tp = cdiv128(len);
+        }
       }
     }
-    if (n > 0) unit(p, row);
+    if (n > 0) unit(p);
   }
 };
 
-// Tile x of the whole sequence as (b, h, rt, tile in the unit), by one warp; total_out: the number of all tiles.
-// first[3]: see find_unit's use in the merge.
-DLLM_DEV int64_t total_tiles(const Params& p) {
+// This CTA's walk[] (see Bars), by one warp.
+DLLM_DEV void make_walk(const Params& p, int* walk) {
+  const Kv8AttnArgs& a = p.a;
   const int lane = threadIdx.x & 31;
-  if (!p.a.lens) return p.a.B * row_tiles(p, 0);
-  int64_t t = 0;
-  for (int b = lane; b < p.a.B; b += 32) t += row_tiles(p, b);
+  const uint32_t mine = lane < a.B ? row_tiles(p, lane) : 0;      // the first 32 batch rows' tiles, read once
+  uint32_t T = mine;
+  for (int b = lane + 32; b < a.B; b += 32) T += row_tiles(p, b);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  return t;
-}
-DLLM_DEV void locate(const Params& p, int64_t x, int& b, int& h, int& rt, int& ta) {
-  const int lane = threadIdx.x & 31;
-  int64_t rem = 0;
-  if (!p.a.lens) {
-    const int64_t per = row_tiles(p, 0);
-    b = (int)(x / per);
-    rem = x - b * per;
-  } else {
-    int64_t base = 0;
-    b = p.a.B - 1;
-    for (int b0 = 0; b0 < p.a.B; b0 += 32) {
-      int64_t v = b0 + lane < p.a.B ? row_tiles(p, b0 + lane) : 0;
+  for (int o = 16; o > 0; o >>= 1) T += __shfl_xor_sync(0xffffffffu, T, o);
+  const Share share(T, p.n_cta);
+  const uint32_t x = share.first(blockIdx.x), n = share.first(blockIdx.x + 1) - x;
+  uint32_t before = 0, rem = 0, in_row = 1;
+  int b = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const uint32_t own = b0 == 0 ? mine : (b0 + lane < a.B ? row_tiles(p, b0 + lane) : 0);
+    uint32_t v = own;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, base + v > x);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        const int64_t before = __shfl_sync(0xffffffffu, v, max(l - 1, 0));
-        b = b0 + l;
-        rem = x - base - (l > 0 ? before : 0);
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, v, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
     }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + v > x);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      in_row = __shfl_sync(0xffffffffu, own, l);
+      rem = x - before - (__shfl_sync(0xffffffffu, v, l) - in_row);
+      b = b0 + l;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, v, 31);
   }
-  const int64_t per_h = row_tiles(p, b) / p.a.Hkv;
-  h = (int)(rem / per_h);
-  rem -= h * per_h;
-  const int tp = cdiv128(kv8::prefix_len(p.a.lens, b, p.a.P));
-  for (rt = 0; rt + 1 < p.n_rt; ++rt) {
-    const int t = max(1, tp + cdiv128(own_keys(p, rt)));
-    if (rem < t) break;
-    rem -= t;
+  if (lane == 0) {
+    const uint32_t per_h = in_row / (uint32_t)a.Hkv;
+    const int h = (int)(rem / per_h);
+    rem -= (uint32_t)h * per_h;
+    const int len = kv8::prefix_len(a.lens, b, a.P), tp = cdiv128(len);
+    int rt = 0;
+    for (; rt + 1 < p.n_rt; ++rt) {
+      const uint32_t t = (uint32_t)max(1, tp + cdiv128(own_keys(p, rt)));
+      if (rem < t) break;
+      rem -= t;
+    }
+    walk[0] = b; walk[1] = h; walk[2] = rt; walk[3] = (int)rem; walk[4] = (int)n; walk[5] = len; walk[6] = (int)T;
   }
-  ta = (int)rem;
 }
 
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
@@ -200,47 +212,39 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
 }
 
 // Four threads quantise a row of 128 bf16 values into two E4M3 parts: this thread's quarter (32 values, src NULL: zeros).
+// The code is kept short: it runs once per unit, and fetching cold instructions is what it costs (a version with a test
+// of every value for infinities took 5 us at the start of the kernel).
 struct Quarter {
   uint4 raw[4];
   DLLM_DEV void load(const __nv_bfloat16* src) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) raw[i] = src ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
   }
-  // largest finite magnitude; bad: whether a value is infinite or NaN
-  DLLM_DEV float amax(bool& bad) const {
-    float m = 0.f;
-    bad = false;
+  // largest magnitude of the row, as bf16 bits (0x7f80 and above: a value is infinite or NaN), over its four threads
+  DLLM_DEV uint32_t amax() const {
+    uint32_t m = 0;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float f[8];
-      bf16x8_to_f32(raw[g], f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = fabsf(f[i]);
-        const bool fin = x < INFINITY;
-        bad |= !fin;
-        m = fin ? fmaxf(m, x) : m;
-      }
+    for (int i = 0; i < 4; ++i) {
+      m = __vmaxu2(m, __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu));
+      m = __vmaxu2(m, __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
     }
-    return m;
+    m = max(m & 0xffffu, m >> 16);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   }
-  // the two parts of each value times inv (a power of two), at the swizzled places of row r of two K-major tiles
+  // the two parts of each value times inv (a power of two, or NaN), at the swizzled places of row r of two K-major tiles
   DLLM_DEV void split(float inv, int r, int quarter, uint8_t* hi_tile, uint8_t* lo_tile) const {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       uint32_t hi[4], lo[4];
-      float f[16];
-      bf16x8_to_f32(raw[2 * g], f);
-      bf16x8_to_f32(raw[2 * g + 1], f + 8);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const uint4& q = raw[2 * g + (i >> 1)];
+        const uint32_t w[2] = {i & 1 ? q.z : q.x, i & 1 ? q.w : q.y};
         uint32_t h2[2], l2[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float a = f[4 * i + 2 * j], b = f[4 * i + 2 * j + 1];
-          // an infinity becomes NaN (E4M3 has none), as the product with it would
-          a = fabsf(a) < INFINITY ? a * inv : __int_as_float(0x7fffffff);
-          b = fabsf(b) < INFINITY ? b * inv : __int_as_float(0x7fffffff);
+          const float a = __uint_as_float(w[j] << 16) * inv, b = __uint_as_float(w[j] & 0xffff0000u) * inv;
           h2[j] = kv8::f32x2_to_e4m3x2(a, b);
           const uint32_t back = kv8::e4m3x2_to_f16x2(h2[j]);
           const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&back));
@@ -255,10 +259,9 @@ struct Quarter {
     }
   }
 };
-DLLM_DEV float max4(float m) {     // over the four threads of a row
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-}
+constexpr uint32_t kInfBits = 0x7f80u;
+DLLM_DEV float qnan() { return __int_as_float(0x7fffffff); }
+DLLM_DEV int bits_exp(uint32_t bf16_bits) { return kv8::scale_exp(__uint_as_float(bf16_bits << 16)); }
 // Address of a unit's query row (NULL past the last).
 DLLM_DEV const __nv_bfloat16* query_row(const Params& p, int b, int h, int rt, int r) {
   const int R = rt * KT + r, qi = R / p.G;
@@ -266,83 +269,99 @@ DLLM_DEV const __nv_bfloat16* query_row(const Params& p, int b, int h, int rt, i
                             (((int64_t)b * p.a.Lq + qi) * p.a.Hq + h * p.G + R - qi * p.G) * 128
                       : nullptr;
 }
-// Q of a unit into shared memory by n threads (t = 0 .. n - 1, n a multiple of 128): parts and row scales.
-DLLM_DEV void stage_q(const Params& p, int b, int h, int rt, int t, int n, uint8_t* sQ, float* qscale,
-                      Quarter* pre /* the first pass's values, already loaded, or NULL */) {
-  for (int r = t >> 2; r < KT; r += n >> 2) {
-    Quarter q;
-    if (pre && r == t >> 2) {
-      q = *pre;
-    } else {
-      const __nv_bfloat16* src = query_row(p, b, h, rt, r);
-      q.load(src ? src + 32 * (t & 3) : nullptr);
-    }
-    bool bad;
-    const int k = kv8::scale_exp(max4(q.amax(bad)));
-    const unsigned any = __ballot_sync(0xffffffffu, bad) >> (threadIdx.x & 28) & 15u;
-    if ((t & 3) == 0) qscale[r] = any ? __int_as_float(0x7fffffff) : kv8::exp2i(k) * (p.a.scale * kLog2e);
+// Q of a unit into shared memory by n threads (t = 0 .. n - 1, n a multiple of 128): parts and row scales. q holds the
+// first pass's values. A row with an infinity or NaN gets the scale NaN, which reaches all its weights.
+DLLM_DEV void stage_q(const Params& p, int b, int h, int rt, int t, int n, uint8_t* sQ, float* qscale, Quarter& q) {
+#pragma unroll 1
+  for (int r = t >> 2;;) {
+    const uint32_t m = q.amax();
+    const int k = m >= kInfBits ? 0 : bits_exp(m);
+    if ((t & 3) == 0) qscale[r] = m >= kInfBits ? qnan() : kv8::exp2i(k) * (p.a.scale * kLog2e);
     q.split(kv8::exp2i(-k), r, t & 3, sQ, sQ + KSTAGE);
+    r += n >> 2;
+    if (r >= KT) break;
+    const __nv_bfloat16* src = query_row(p, b, h, rt, r);
+    q.load(src ? src + 32 * (t & 3) : nullptr);
   }
 }
+// 32 values of a unit's query row (t >> 2), by the thread's quarter.
+DLLM_DEV void load_q(const Params& p, int b, int h, int rt, int t, Quarter& q) {
+  const __nv_bfloat16* src = query_row(p, b, h, rt, t >> 2);
+  q.load(src ? src + 32 * (t & 3) : nullptr);
+}
 
-// This thread's 64 columns of S: the largest x = S c + lv over the visible ones (the first lim).
-template <bool MASK>
-DLLM_DEV float tile_max(const float* v, int lim, float rowc, const float4* run, int rstep) {
+// Factor and offset of a run's exponents: x = S c + d. c is kept above 0 (a zero K scale), so that a masked score of -inf
+// stays -inf; NaN stays NaN.
+DLLM_DEV float run_factor(float rowc, const float4& rs) {
+  const float c = rowc * rs.x;
+  return c < 1e-30f ? 1e-30f : c;
+}
+// 64 columns of S, the first lim of them visible.
+DLLM_DEV void mask_scores(float* v, int lim) {
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = i < lim ? v[i] : -INFINITY;
+}
+// The largest x = S c + lv of the 64 columns.
+DLLM_DEV float tile_max(const float* v, float rowc, const float4* run, int rstep) {
   float mt = -INFINITY;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const float4 rs = run[u * rstep];
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float x = v[16 * u + i];
-      if (!MASK || 16 * u + i < lim) m = fmaxf(m, x);
-    }
-    mt = fmaxf(mt, fmaf(m, rowc * rs.x, rs.y));
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, v[16 * u + i]);
+    mt = fmaxf(mt, fmaf(m, run_factor(rowc, rs), rs.y));
   }
   return mt;
 }
-// P of the 64 columns as f16 pairs; returns the sum of the weights with the V scales divided out.
-template <bool MASK>
-DLLM_DEV float tile_exp(const float* v, int lim, float rowc, const float4* run, int rstep, float shift, uint32_t* pk) {
+DLLM_DEV void tmem_st8(uint32_t at, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// P of the 64 columns as f16 pairs, to 32 columns of TMEM; returns the sum of the weights with the V scales divided out.
+DLLM_DEV float tile_exp(const float* v, float rowc, const float4* run, int rstep, float shift, uint32_t at) {
   float l = 0.f;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const float4 rs = run[u * rstep];
-    const float c = rowc * rs.x, d = rs.y + shift;
+    const float c = run_factor(rowc, rs), d = rs.y + shift;
     const uint64_t c2 = pk2(c, c), d2 = pk2(d, d);
     uint64_t s2 = pk2(0.f, 0.f);
+    uint32_t pk[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float x0, x1;
       upk2(fma2(pk2(v[16 * u + 2 * i], v[16 * u + 2 * i + 1]), c2, d2), x0, x1);
-      float e0 = ex2(x0), e1 = ex2(x1);
-      if (MASK) {
-        if (16 * u + 2 * i >= lim) e0 = 0.f;
-        if (16 * u + 2 * i + 1 >= lim) e1 = 0.f;
-      }
-      pk[8 * u + i] = f16x2(e0, e1);
+      const float e0 = ex2(x0), e1 = ex2(x1);
+      pk[i] = f16x2(e0, e1);
       s2 = add2(s2, pk2(e0, e1));
     }
     float s0, s1;
     upk2(s2, s0, s1);
     l = fmaf(s0 + s1, rs.z, l);
+    tmem_st8(at + 8 * u, pk);
   }
   return l;
 }
-// Barrier of the two warps that share 32 rows, with the OR of a predicate.
-DLLM_DEV bool pair_or(int id, bool pred) {
-  uint32_t r;
+// TMEM rows 16 columns at a time: the vectors of wider accesses need aligned runs of registers, which fragment the file
+// beside 64 scores (32-column accesses made the softmax spill).
+DLLM_DEV void tmem_ld16_issue(uint32_t at, uint32_t* r) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred p, %2, 64, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)pred), "r"(id)
-      : "memory");
-  return r != 0;
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
 }
+DLLM_DEV void load_scores(uint32_t at, float* v) {      // 64 columns
+  uint32_t r[64];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld16_issue(at + 16 * c, r + 16 * c);
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+DLLM_DEV void named_bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 DLLM_DEV void arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar)), "r"(n) : "memory");
 }
@@ -376,11 +395,12 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       tc::mbar_init(&bar.w_full[i], 4);
       tc::mbar_init(&bar.w_empty[i], 1);
       tc::mbar_init(&bar.s_full[i], 1);
-      tc::mbar_init(&bar.p_ready[i], 8);
+      tc::mbar_init(&bar.s_full[NB + i], 1);
+      tc::mbar_init(&bar.p_ready[i], 4);
     }
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&bar.r_full[i], 1);
-      tc::mbar_init(&bar.r_empty[i], 8);
+      tc::mbar_init(&bar.r_empty[i], 4);
     }
     tc::mbar_init(&bar.o_free, 8);
     tc::mbar_init(&bar.done, 1);
@@ -391,34 +411,27 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   pdl_trigger();
   if (warp == 0) {
     pdl_wait();        // the lengths may come from the kernel before
-    const int64_t T = total_tiles(p);
-    const int64_t x0 = blockIdx.x * T / p.n_cta, x1 = (blockIdx.x + 1) * T / p.n_cta;
-    int b = 0, h = 0, rt = 0, ta = 0;
-    if (x1 > x0) locate(p, x0, b, h, rt, ta);
-    if (lane == 0) {
-      bar.walk[0] = b; bar.walk[1] = h; bar.walk[2] = rt; bar.walk[3] = ta; bar.walk[4] = (int)(x1 - x0);
-      bar.walk[5] = (int)T;
-    }
+    make_walk(p, bar.walk);
   }
   __syncthreads();
   pdl_wait();
   volatile int* abort_flag = &bar.abort_flag;
   const uint32_t tS = bar.tmem_base, tO = bar.tmem_base + NB * 128;
-  Walk w;
-  w.start(p, bar.walk);
   auto arrive = [&](uint64_t* b) {       // once for the warp, after all its lanes
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(b);
   };
 
-  // The four warpgroups launch with 128 registers a thread each and go to 104, 152, 152, 104 (the same sum): a softmax
-  // thread holds 64 scores beside what the rare rescale of O needs. Nothing may spill: shared memory leaves the L1 next to
-  // nothing, so local memory is L2 (a build with 424 bytes of spills took 3 times as long).
+  // The four warpgroups launch with 128 registers a thread each and go to 120, 136, 136, 120 (the same sum), which is where
+  // nothing spills. Shared memory leaves the L1 next to nothing, so a spill goes to L2: builds with a few hundred bytes of
+  // them took up to 3 times as long.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA: codes of the prefix tiles
     if (tc::elect_one()) {
+      Walk w;
+      w.start(p, bar.walk);
       const uint64_t pol = p.reuse ? tc::policy_evict_last() : tc::policy_evict_first();
       uint32_t ks = 0, vs = 0;      // slots of the K and V rings so far
       uint32_t kq = 0, vq = 0;      // one past the last slot that this thread filled (for the drain)
@@ -465,6 +478,8 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
     if (tc::elect_one()) {
+      Walk w;
+      w.start(p, bar.walk);
       const uint32_t id_s = (1u << 4) | ((KT >> 3) << 17) | ((KT >> 4) << 24);                // E4M3 x E4M3 -> f32
       const uint32_t id_o = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((KT >> 4) << 24);  // f16 x f16, B MN-major
       const uint64_t dQ = tc::sdesc_k128(tc::smem_u32(sQ)), dK = tc::sdesc_k128(tc::smem_u32(sK));
@@ -472,7 +487,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       // the S products run up to NB tiles ahead of P V, with a walk of their own
       Walk ws = w;
       int ts = w.ta;               // next tile of ws
-      uint32_t k = 0, kph = 0, sb = 0, seg_s = 0;
+      uint32_t k = 0, kph = 0, s6 = 0, seg_s = 0;
       bool q_ready = false, ok = true;
       auto issue_s = [&]() -> bool {
         if (!q_ready) {
@@ -480,7 +495,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           q_ready = true;
         }
         const bool own = ts >= ws.tp && ts < ws.tp + cdiv128(ws.own);
-        const uint32_t d = tS + sb * 128;
+        const uint32_t d = tS + (s6 >= NB ? s6 - NB : s6) * 128;
         for (int part = 0; part < (own ? 2 : 1); ++part) {
           if (!wait_bar(&bar.k_full[k], kph, abort_flag, a.status, ST_TIMEOUT_MMA)) return false;
           tc::fence_after_sync();
@@ -494,8 +509,8 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             kph ^= 1;
           }
         }
-        tc::mma_commit(&bar.s_full[sb]);
-        sb = sb == NB - 1 ? 0 : sb + 1;
+        tc::mma_commit(&bar.s_full[s6]);
+        s6 = s6 == 2 * NB - 1 ? 0 : s6 + 1;
         if (++ts == ws.end()) {
           tc::mma_commit(&bar.q_empty);
           ws.next(p);
@@ -544,6 +559,8 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   } else {
     // ------------------------------------------------------------------ scales of the prefix tiles
     // lanes 0-7 K, 8-15 V, one per 16 keys; the next of this warp's tiles is loaded while the last waits for its slot
+    Walk w;
+    w.start(p, bar.walk);
     const int64_t runs = (a.cap + a.S - 1) / a.S;
     uint32_t pt = 0;
     float held = 0.f;
@@ -574,18 +591,19 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   }
   } else if (warp >= 12) {
     // ------------------------------------------------------------------ converters
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    Walk w;
+    w.start(p, bar.walk);
     const int ct = tid - 384;
     const uint32_t cw = warp - 12;
     uint32_t k = 0, v = 0, vph = 0, g = 0, wph = 1, seg = 0, granted = 0;
     for (; w.n > 0; w.next(p), ++seg) {
       const int64_t bh = (int64_t)w.b * a.Hkv + w.h;
       if (seg > 0) {   // the first unit's Q is staged by the softmax warps, which have nothing to do yet
-        Quarter pre;
-        const __nv_bfloat16* src = query_row(p, w.b, w.h, w.rt, ct >> 2);
-        pre.load(src ? src + 32 * (ct & 3) : nullptr);
+        Quarter q;
+        load_q(p, w.b, w.h, w.rt, ct, q);      // before the wait for the previous unit's last S
         wait_bar(&bar.q_empty, (seg - 1) & 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
-        stage_q(p, w.b, w.h, w.rt, ct, 128, sQ, bar.qscale, &pre);
+        stage_q(p, w.b, w.h, w.rt, ct, 128, sQ, bar.qscale, q);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) arrive_n(&bar.q_full, 2);
@@ -625,24 +643,27 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           // own rows (none at all in a unit without keys): four threads per key, 32 keys at a time
           const int j0 = (t - w.tp) * KT, n = min(KT, w.own - j0), parts = n > 0 ? 2 : 1;
           const int64_t at = (bh * a.cap_own + j0) * 128 + 32 * (ct & 3);
-          float mk = 0.f, mv = 0.f;
-          for (int r = ct >> 2; r < n; r += 32) {
+          // largest finite magnitudes (a row with an infinity or NaN counts as 0: K makes all its codes NaN)
+          uint32_t mk = 0, mv = 0;
+#pragma unroll 1
+          for (int r = ct >> 2; r < KT; r += 32) {
             Quarter q;
-            bool bad;
-            q.load(static_cast<const __nv_bfloat16*>(a.k_own) + at + r * 128);
-            mk = fmaxf(mk, q.amax(bad));
-            q.load(static_cast<const __nv_bfloat16*>(a.v_own) + at + r * 128);
-            mv = fmaxf(mv, q.amax(bad));
+            q.load(r < n ? static_cast<const __nv_bfloat16*>(a.k_own) + at + r * 128 : nullptr);
+            const uint32_t x = q.amax();
+            q.load(r < n ? static_cast<const __nv_bfloat16*>(a.v_own) + at + r * 128 : nullptr);
+            const uint32_t y = q.amax();
+            mk = max(mk, x < kInfBits ? x : 0u);
+            mv = max(mv, y < kInfBits ? y : 0u);
           }
-          mk = warp_max(mk);
-          mv = warp_max(mv);
+          mk = __reduce_max_sync(0xffffffffu, mk);
+          mv = __reduce_max_sync(0xffffffffu, mv);
           if (lane == 0) {
             bar.red[0][cw] = mk;
             bar.red[1][cw] = mv;
           }
           tc::named_bar_sync(kBarConv, 128);
-          const int ek = kv8::scale_exp(fmaxf(fmaxf(bar.red[0][0], bar.red[0][1]), fmaxf(bar.red[0][2], bar.red[0][3])));
-          const int ev = kv8::scale_exp(fmaxf(fmaxf(bar.red[1][0], bar.red[1][1]), fmaxf(bar.red[1][2], bar.red[1][3])));
+          const int ek = bits_exp(max(max(bar.red[0][0], bar.red[0][1]), max(bar.red[0][2], bar.red[0][3])));
+          const int ev = bits_exp(max(max(bar.red[1][0], bar.red[1][1]), max(bar.red[1][2], bar.red[1][3])));
           if (ct == 0) bar.run_own[g] = make_float4(kv8::exp2i(ek), (float)ev, kv8::exp2i(-ev), 0.f);
           const uint32_t k0 = k, k1 = parts == 2 ? (k + 1) % NK : k;
           for (int i = 0; i < parts; ++i) {
@@ -651,10 +672,11 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             granted ^= 1u << kk;
           }
           const float ik = kv8::exp2i(-ek), iv = kv8::exp2i(-ev);
+#pragma unroll 1
           for (int r = ct >> 2; r < KT; r += 32) {
             Quarter q;
             q.load(r < n ? static_cast<const __nv_bfloat16*>(a.k_own) + at + r * 128 : nullptr);
-            q.split(ik, r, ct & 3, sK + k0 * KSTAGE, sK + k1 * KSTAGE);
+            q.split(q.amax() < kInfBits ? ik : qnan(), r, ct & 3, sK + k0 * KSTAGE, sK + k1 * KSTAGE);
             q.load(r < n ? static_cast<const __nv_bfloat16*>(a.v_own) + at + r * 128 : nullptr);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -681,12 +703,16 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     }
   } else {
     // ------------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, pair = kBarPair + (warp & 3);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+    Walk w;
+    w.start(p, bar.walk);
+    const int grp = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, pair = kBarPair + (warp & 3);
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    uint32_t it = 0, g = 0, ph = 0, pt = 0, seg = 0;
+    uint32_t it = 0, g = 0, ph = 0, s6 = 0, sph = 0, pt = 0, seg = 0;
     if (w.n > 0) {
-      stage_q(p, w.b, w.h, w.rt, tid - 128, 256, sQ, bar.qscale, nullptr);
+      Quarter q;
+      load_q(p, w.b, w.h, w.rt, tid - 128, q);
+      stage_q(p, w.b, w.h, w.rt, tid - 128, 256, sQ, bar.qscale, q);
       fence_async_smem();
       arrive(&bar.q_full);
     }
@@ -698,45 +724,58 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       wait_bar(&bar.q_full, seg & 1, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
       const float rowc = bar.qscale[row];
       arrive(&bar.q_empty);
-      float mg = -INFINITY, l = 0.f;
-      for (int t = w.ta; t < w.end(); ++t, ++it) {
+      float mg = -INFINITY, l = 0.f;      // the sum of this group's tiles, relative to mg
+      const int t_end = w.end();
+      for (int t = w.ta; t < t_end; ++t, ++it) {
         const bool pre = t < w.tp;
-        const uint32_t rs = pt & 3;
-        const int lim = (pre ? w.len - t * KT : own_lim - (t - w.tp) * KT) - 64 * half;
-        if (pre)
-          wait_bar(&bar.r_full[rs], (pt >> 2) & 1, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
-        else
-          wait_bar(&bar.w_full[g], ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
-        wait_bar(&bar.s_full[g], ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
-        if (warp_live) {
-          const float4* run = pre ? &bar.run[rs][4 * half] : &bar.run_own[g];
-          const int rstep = pre ? 1 : 0;
-          const bool fast = __all_sync(0xffffffffu, lim >= 64);
-          tc::fence_after_sync();
-          const uint32_t tSg = tS + g * 128 + lane_off;
-          float v[64];
-          tmem_ld64(tSg + 64 * half, v);
-          const float mt = fast ? tile_max<false>(v, lim, rowc, run, rstep) : tile_max<true>(v, lim, rowc, run, rstep);
-          // also orders the other warp's loads of S before this one's P, which overwrites them
-          if (pair_or(pair, mt > mg + kRescale)) {
-            bar.xm[it & 1][half][row] = mt;
-            tc::named_bar_sync(pair, 64);
-            const float mm = fmaxf(bar.xm[it & 1][0][row], bar.xm[it & 1][1][row]);
-            float alpha = 1.f;
-            if (mm > mg + kRescale) {
-              alpha = mg == -INFINITY ? 1.f : ex2(mg - mm);
-              mg = mm;
+        if ((int)(it & 1) == grp) {
+          const uint32_t rs = pt & 3;
+          const int lim = pre ? w.len - t * KT : own_lim - (t - w.tp) * KT;
+          // every barrier here is at most one phase behind what is waited for: this group's last tile was it - 2, after
+          // the other's it - 3, and S of this tile was issued behind P V of it - 3
+          wait_bar(&bar.s_full[s6], sph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+          if (pre)
+            wait_bar(&bar.r_full[rs], (pt >> 2) & 1, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+          else
+            wait_bar(&bar.w_full[g], ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+          if (warp_live) {
+            const float4* run = pre ? bar.run[rs] : &bar.run_own[g];
+            const int rstep = pre ? 1 : 0;
+            tc::fence_after_sync();
+            const uint32_t tSg = tS + g * 128 + lane_off;
+            const bool partly = !__all_sync(0xffffffffu, lim >= KT);
+            // columns [64, 128) for their maximum alone, then [0, 64), kept for their weights; P takes half the columns
+            // of the scores it replaces, so the upper half is read again afterwards
+            float v[64];
+            load_scores(tSg + 64, v);
+            if (partly) mask_scores(v, lim - 64);
+            float mt = tile_max(v, rowc, run + 4 * rstep, rstep);
+            load_scores(tSg, v);
+            if (partly) mask_scores(v, lim);
+            mt = fmaxf(mt, tile_max(v, rowc, run, rstep));
+            float prev = -INFINITY;
+            if (t > w.ta) {
+              tc::named_bar_sync(pair + 4 * (grp ^ 1), 64);
+              prev = bar.ref[(it & 1) ^ 1][row];
             }
-            l *= alpha;
+            const float now = mt > prev + kRescale ? mt : prev;
+            if (t + 1 < t_end) {
+              bar.ref[it & 1][row] = now;
+              named_bar_arrive(pair + 4 * grp, 64);
+            }
+            if (mg != now) {
+              l *= ex2(mg - now);
+              mg = now;
+            }
+            const float alpha = prev == now || prev == -INFINITY ? 1.f : ex2(prev - now);
             if (t > w.ta && __any_sync(0xffffffffu, alpha != 1.f)) {
-              // O holds the unit's previous tiles once the last P V completes. S of this tile is complete, so the P V
-              // three tiles ago, issued before it, is too: the last one's barrier is at most one phase behind.
+              // O holds the unit's tiles before this one once the last P V completes
               wait_bar(&bar.w_empty[g == 0 ? NB - 1 : g - 1], g == 0 ? ph ^ 1 : ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
               __syncwarp();
               tc::fence_after_sync();
 #pragma unroll 1
-              for (int c = 0; c < 8; ++c) {      // 8 columns at a time: the scores stay in registers meanwhile
-                const uint32_t at = tO + 64 * half + 8 * c + lane_off;
+              for (int c = 0; c < 16; ++c) {      // 8 columns at a time: the scores stay in registers meanwhile
+                const uint32_t at = tO + 8 * c + lane_off;
                 uint32_t x[8];
                 asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
                              "tcgen05.wait::ld.sync.aligned;"
@@ -751,31 +790,36 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                              : "memory");
               }
             }
+            const float shift = kOff - (mg == -INFINITY ? 0.f : mg);
+            l += tile_exp(v, rowc, run, rstep, shift, tSg);
+            load_scores(tSg + 64, v);
+            if (partly) mask_scores(v, lim - 64);
+            l += tile_exp(v, rowc, run + 4 * rstep, rstep, shift, tSg + 32);
+            tc::tmem_st_wait();
+            tc::fence_before_sync();
           }
-          const float shift = kOff - (mg == -INFINITY ? 0.f : mg);
-          uint32_t pk[32];
-          l += fast ? tile_exp<false>(v, lim, rowc, run, rstep, shift, pk) : tile_exp<true>(v, lim, rowc, run, rstep, shift, pk);
-          tc::tmem_st32(tSg + 32 * half, pk);
-          tc::tmem_st_wait();
-          tc::fence_before_sync();
+          arrive(&bar.p_ready[g]);
+          if (pre && lane == 0) tc::mbar_arrive(&bar.r_empty[rs]);
         }
-        arrive(&bar.p_ready[g]);
-        if (pre) {
-          if (lane == 0) tc::mbar_arrive(&bar.r_empty[rs]);
-          ++pt;
-        }
+        pt += pre;
         if (++g == NB) {
           g = 0;
           ph ^= 1;
         }
+        if (++s6 == 2 * NB) {
+          s6 = 0;
+          sph ^= 1;
+        }
       }
-      // the unit's last P V
-      wait_bar(&bar.w_empty[g == 0 ? NB - 1 : g - 1], g == 0 ? ph ^ 1 : ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
       const bool whole = w.ta == 0 && w.end() == w.tiles;
+      bar.ml[seg & 1][grp][row] = make_float2(mg, l);
+      tc::named_bar_sync(pair + 8, 64);
+      // the unit's last P V (the group of its last tile, now here too, has seen the S behind the one three before it)
+      wait_bar(&bar.w_empty[g == 0 ? NB - 1 : g - 1], g == 0 ? ph ^ 1 : ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
       if (warp_live) {
-        bar.xl[seg & 1][half][row] = l;
-        tc::named_bar_sync(pair, 64);
-        const float L = bar.xl[seg & 1][0][row] + bar.xl[seg & 1][1][row];
+        const float2 x0 = bar.ml[seg & 1][0][row], x1 = bar.ml[seg & 1][1][row];
+        mg = fmaxf(x0.x, x1.x);           // what O is relative to: the reference never decreases
+        const float L = (x0.x == mg ? x0.y : x0.y * ex2(x0.x - mg)) + (x1.x == mg ? x1.y : x1.y * ex2(x1.x - mg));
         const float inv = L == 0.f ? 0.f : 1.0f / L;
         const bool put = !*abort_flag && live;
         const int64_t qh = ((int64_t)w.b * a.Lq + qi) * a.Hq + w.h * p.G + (live ? R - qi * p.G : 0);
@@ -784,7 +828,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         tc::fence_after_sync();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int col = 64 * half + 32 * c;
+          const int col = 64 * grp + 32 * c;
           float o[32];
           tmem_ld32(tO + col + lane_off, o);
           if (put && whole) {
@@ -807,16 +851,16 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           __syncwarp();
         }
         tc::fence_before_sync();
-        if (put && half == 0) {
+        if (put && grp == 0) {
           if (!whole) part[32 * KT + row] = make_float4(mg, L, 0.f, 0.f);
           else if (a.lse_out) a.lse_out[qh] = L == 0.f ? -INFINITY : (mg - kOff + log2f(L)) * kLn2;
         }
       }
       if (tid == 128 && w.ta == 0) {
-        // for the join: CTA c owns tiles [c T / n, (c + 1) T / n), so tile x is in c = ((x + 1) n - 1) / T
-        const int64_t T = bar.walk[5], s = (blockIdx.x + 1) * T / p.n_cta - w.n, e = s + w.tiles;
-        const int c1 = (int)((e * p.n_cta - 1) / T), share = T < p.n_cta ? w.tiles : c1 - (int)blockIdx.x + 1;
-        p.span[((int64_t)w.b * a.Hkv + w.h) * p.n_rt + w.rt] = make_int4((int)s, whole ? 0 : share, (int)T, 0);
+        const Share share((uint32_t)bar.walk[6], p.n_cta);
+        const uint32_t first = share.first(blockIdx.x + 1) - (uint32_t)w.n;
+        const int last = (int)share.cta_of(first + (uint32_t)w.tiles - 1);
+        p.span[((int64_t)w.b * a.Hkv + w.h) * p.n_rt + w.rt] = make_int2((int)blockIdx.x, last);
       }
       arrive(&bar.o_free);
     }
@@ -836,24 +880,20 @@ __global__ void __launch_bounds__(KT) attn_kv8_merge_kernel(const __grid_constan
   const Kv8AttnArgs& a = p.a;
   const int row = threadIdx.x, part_col = blockIdx.x % (128 / kMergeCols);
   const int64_t unit = blockIdx.x / (128 / kMergeCols);
-  const int4 sp = p.span[unit];
-  const int rt = (int)(unit % p.n_rt), R = rt * KT + row;
-  if (sp.y == 0 || R >= p.n_rows) return;
-  const int64_t T = sp.z;
-  const int c0 = (int)(((int64_t)(sp.x + 1) * p.n_cta - 1) / T);
-  // the k-th CTA of the unit; with more CTAs than tiles some own none, and every tile has a CTA of its own
+  const int2 sp = p.span[unit];
+  const int rt = (int)(unit % p.n_rt), R = rt * KT + row, n = sp.y - sp.x + 1;
+  if (n == 1 || R >= p.n_rows) return;
   auto slot = [&](int k) {
-    const int c = T < p.n_cta ? (int)(((int64_t)(sp.x + k + 1) * p.n_cta - 1) / T) : c0 + k;
-    return reinterpret_cast<const float4*>(p.part) + ((int64_t)c * 2 + (k == 0 ? 1 : 0)) * (kPart / 4);
+    return reinterpret_cast<const float4*>(p.part) + ((int64_t)(sp.x + k) * 2 + (k == 0 ? 1 : 0)) * (kPart / 4);
   };
   float M = -INFINITY;
 #pragma unroll 4
-  for (int k = 0; k < sp.y; ++k) M = fmaxf(M, slot(k)[32 * KT + row].x);
+  for (int k = 0; k < n; ++k) M = fmaxf(M, slot(k)[32 * KT + row].x);
   float L = 0.f, o[kMergeCols];
 #pragma unroll
   for (int i = 0; i < kMergeCols; ++i) o[i] = 0.f;
 #pragma unroll 4
-  for (int k = 0; k < sp.y; ++k) {
+  for (int k = 0; k < n; ++k) {
     const float4* s = slot(k);
     const float4 ml = s[32 * KT + row];
     const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
@@ -920,7 +960,7 @@ int64_t own_tiles_sum(const Kv8AttnArgs& a, int n_rt, int G) {
 // Partial results of every CTA, then the units' spans.
 size_t attn_kv8_tc_workspace_bytes(int B, int Lq, int Hq, int Hkv) {
   const size_t units = (size_t)B * Hkv * (((size_t)Lq * (Hq / Hkv) + KT - 1) / KT);
-  return (size_t)num_sms() * 2 * kPart * sizeof(float) + units * sizeof(int4);
+  return (size_t)num_sms() * 2 * kPart * sizeof(float) + units * sizeof(int2);
 }
 
 int launch_attn_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
@@ -931,7 +971,7 @@ int launch_attn_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
   p.n_rt = (p.n_rows + KT - 1) / KT;
   p.own_sum = own_tiles_sum(a, p.n_rt, p.G);
   p.part = static_cast<float*>(a.ws);
-  p.span = reinterpret_cast<int4*>(p.part + (size_t)num_sms() * 2 * kPart);
+  p.span = reinterpret_cast<int2*>(p.part + (size_t)num_sms() * 2 * kPart);
   p.reuse = p.n_rt > 1;
   // most tiles there can be (lengths may be shorter): no more CTAs than those
   const int64_t tp = (a.P + KT - 1) / KT;
