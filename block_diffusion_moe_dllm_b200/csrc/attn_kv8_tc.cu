@@ -296,16 +296,19 @@ DLLM_DEV float run_factor(float rowc, const float4& rs) {
   const float c = rowc * rs.x;
   return c < 1e-30f ? 1e-30f : c;
 }
-// 64 columns of S, the first lim of them visible.
-DLLM_DEV void mask_scores(float* v, int lim) {
+// 32 columns of S in one row, the first lim of them visible if partly.
+DLLM_DEV void load_scores(uint32_t at, bool partly, int lim, float* v) {
+  tmem_ld32(at, v);
+  if (partly) {
 #pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = i < lim ? v[i] : -INFINITY;
+    for (int i = 0; i < 32; ++i) v[i] = i < lim ? v[i] : -INFINITY;
+  }
 }
-// The largest x = S c + lv of the 64 columns.
-DLLM_DEV float tile_max(const float* v, float rowc, const float4* run, int rstep) {
+// The largest x = S c + lv of 32 columns.
+DLLM_DEV float scores_max(const float* v, float rowc, const float4* run, int rstep) {
   float mt = -INFINITY;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
+  for (int u = 0; u < 2; ++u) {
     const float4 rs = run[u * rstep];
     float m = -INFINITY;
 #pragma unroll
@@ -314,52 +317,34 @@ DLLM_DEV float tile_max(const float* v, float rowc, const float4* run, int rstep
   }
   return mt;
 }
-DLLM_DEV void tmem_st8(uint32_t at, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-// P of the 64 columns as f16 pairs, to 32 columns of TMEM; returns the sum of the weights with the V scales divided out.
-DLLM_DEV float tile_exp(const float* v, float rowc, const float4* run, int rstep, float shift, uint32_t at) {
+// P of 32 columns as f16 pairs, to 16 columns of TMEM; returns the sum of the weights with the V scales divided out.
+DLLM_DEV float scores_exp(const float* v, float rowc, const float4* run, int rstep, float shift, uint32_t at) {
   float l = 0.f;
+  uint32_t pk[16];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
+  for (int u = 0; u < 2; ++u) {
     const float4 rs = run[u * rstep];
     const float c = run_factor(rowc, rs), d = rs.y + shift;
     const uint64_t c2 = pk2(c, c), d2 = pk2(d, d);
     uint64_t s2 = pk2(0.f, 0.f);
-    uint32_t pk[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float x0, x1;
       upk2(fma2(pk2(v[16 * u + 2 * i], v[16 * u + 2 * i + 1]), c2, d2), x0, x1);
       const float e0 = ex2(x0), e1 = ex2(x1);
-      pk[i] = f16x2(e0, e1);
+      pk[8 * u + i] = f16x2(e0, e1);
       s2 = add2(s2, pk2(e0, e1));
     }
     float s0, s1;
     upk2(s2, s0, s1);
     l = fmaf(s0 + s1, rs.z, l);
-    tmem_st8(at + 8 * u, pk);
   }
-  return l;
-}
-// TMEM rows 16 columns at a time: the vectors of wider accesses need aligned runs of registers, which fragment the file
-// beside 64 scores (32-column accesses made the softmax spill).
-DLLM_DEV void tmem_ld16_issue(uint32_t at, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(at));
-}
-DLLM_DEV void load_scores(uint32_t at, float* v) {      // 64 columns
-  uint32_t r[64];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) tmem_ld16_issue(at + 16 * c, r + 16 * c);
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7]), "r"(pk[8]),
+      "r"(pk[9]), "r"(pk[10]), "r"(pk[11]), "r"(pk[12]), "r"(pk[13]), "r"(pk[14]), "r"(pk[15])
+      : "memory");
+  return l;
 }
 DLLM_DEV void named_bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 DLLM_DEV void arrive_n(uint64_t* bar, uint32_t n) {
@@ -486,7 +471,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       const uint64_t dW = sdesc_mn128(tc::smem_u32(sW), VCHUNK);      // addresses step by bytes >> 4
       // the S products run up to NB tiles ahead of P V, with a walk of their own
       Walk ws = w;
-      int ts = w.ta;               // next tile of ws
+      int ts = w.ta, te = w.n > 0 ? w.end() : 0;      // next tile of ws, end of its tiles
       uint32_t k = 0, kph = 0, s6 = 0, seg_s = 0;
       bool q_ready = false, ok = true;
       auto issue_s = [&]() -> bool {
@@ -494,7 +479,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           if (!wait_bar(&bar.q_full, seg_s & 1, abort_flag, a.status, ST_TIMEOUT_MMA)) return false;
           q_ready = true;
         }
-        const bool own = ts >= ws.tp && ts < ws.tp + cdiv128(ws.own);
+        const bool own = ts >= ws.tp && ws.own > 0;
         const uint32_t d = tS + (s6 >= NB ? s6 - NB : s6) * 128;
         for (int part = 0; part < (own ? 2 : 1); ++part) {
           if (!wait_bar(&bar.k_full[k], kph, abort_flag, a.status, ST_TIMEOUT_MMA)) return false;
@@ -511,10 +496,11 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         tc::mma_commit(&bar.s_full[s6]);
         s6 = s6 == 2 * NB - 1 ? 0 : s6 + 1;
-        if (++ts == ws.end()) {
+        if (++ts == te) {
           tc::mma_commit(&bar.q_empty);
           ws.next(p);
           ts = 0;
+          te = ws.n > 0 ? ws.end() : 0;
           ++seg_s;
           q_ready = false;
         }
@@ -615,7 +601,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           const int n = min(KT, w.len - t * KT);
           wait_bar(&bar.v_full[v], vph, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
           const uint8_t* src = sV + v * KSTAGE;
-#pragma unroll
+#pragma unroll 2
           for (int i = 0; i < 8; ++i) {
             const int id = i * 128 + ct, key = id >> 3, e = id & 7;      // 16 codes: key, columns 16 e ..
             uint4 u = *reinterpret_cast<const uint4*>(src + id * 16);
@@ -744,15 +730,16 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             tc::fence_after_sync();
             const uint32_t tSg = tS + g * 128 + lane_off;
             const bool partly = !__all_sync(0xffffffffu, lim >= KT);
-            // columns [64, 128) for their maximum alone, then [0, 64), kept for their weights; P takes half the columns
-            // of the scores it replaces, so the upper half is read again afterwards
-            float v[64];
-            load_scores(tSg + 64, v);
-            if (partly) mask_scores(v, lim - 64);
-            float mt = tile_max(v, rowc, run + 4 * rstep, rstep);
-            load_scores(tSg, v);
-            if (partly) mask_scores(v, lim);
-            mt = fmaxf(mt, tile_max(v, rowc, run, rstep));
+            // the row of S is read twice, 32 columns at a time, for its maximum and for its weights: loops this short stay
+            // in the instruction caches, which four kinds of warps share (the same code unrolled over 128 columns took
+            // 10 % longer). P takes half the columns of the scores that it replaces, all read by then.
+            float mt = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float v[32];
+              load_scores(tSg + 32 * c, partly, lim - 32 * c, v);
+              mt = fmaxf(mt, scores_max(v, rowc, run + 2 * c * rstep, rstep));
+            }
             float prev = -INFINITY;
             if (t > w.ta) {
               tc::named_bar_sync(pair + 4 * (grp ^ 1), 64);
@@ -791,10 +778,12 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
               }
             }
             const float shift = kOff - (mg == -INFINITY ? 0.f : mg);
-            l += tile_exp(v, rowc, run, rstep, shift, tSg);
-            load_scores(tSg + 64, v);
-            if (partly) mask_scores(v, lim - 64);
-            l += tile_exp(v, rowc, run + 4 * rstep, rstep, shift, tSg + 32);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float v[32];
+              load_scores(tSg + 32 * c, partly, lim - 32 * c, v);
+              l += scores_exp(v, rowc, run + 2 * c * rstep, rstep, shift, tSg + 16 * c);
+            }
             tc::tmem_st_wait();
             tc::fence_before_sync();
           }
