@@ -369,6 +369,8 @@ size_t attn_kv8_workspace_bytes(int B, int Lq, int Hq, int Hkv, int d, int P, in
 int launch_attn_kv8(const Kv8AttnArgs& a, cudaStream_t s) {
   return a.dtype == DLLM_BF16 ? launch_attn_kv8_tc(a, s) : launch_attn_kv8_simt(a, s);
 }
-int launch_attn_mass_kv8(const Kv8AttnArgs& a, cudaStream_t s) { return launch_attn_mass_kv8_simt(a, s); }
+int launch_attn_mass_kv8(const Kv8AttnArgs& a, cudaStream_t s) {
+  return a.dtype == DLLM_BF16 ? launch_attn_mass_kv8_tc(a, s) : launch_attn_mass_kv8_simt(a, s);
+}
 
 }  // namespace dllm

@@ -914,6 +914,254 @@ __global__ void __launch_bounds__(KT) attn_kv8_merge_kernel(const __grid_constan
   if (part_col == 0 && a.lse_out) a.lse_out[qh] = L == 0.f ? -INFINITY : (M - kOff + log2f(L)) * kLn2;
 }
 
+// ------------------------------------------------------------------------------------------------ attention weight
+// mass[j] (+)= sum over the query rows R of 2^(S[R, j] c - lse2[R]). The product is transposed, S^T = K Q^T: keys are the
+// rows of the accumulator, so a thread owns a key and adds its row up in registers, with no sum across threads and no
+// atomics. The queries of a row tile share one power-of-two scale, so that the factor c = k_scale 2^k scale log2(e) is
+// the thread's own; lse2 comes from shared memory. Key tiles are dealt to the CTAs like the attention's; a CTA goes over
+// its tiles of a (b, kv head) once per row tile of the queries (more than one: K comes from L2 after the first time).
+// Bound by the exponentials: 128 x 128 per key tile and row tile, 1024 clocks, against 512 of MMAs and 710 of HBM.
+// Roles: warp 0 TMA, warp 1 MMA, warps 4-7 and 8-11 alternate key tiles, warps 12-15 stage the queries.
+constexpr int MK = 5, MS = 4;              // stages of the K ring, S buffers
+struct MassBars {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[MK], k_empty[MK];
+  uint64_t s_full[MS], s_empty[MS];
+  uint64_t done;
+  uint32_t tmem_base;
+  int abort_flag;
+  int walk[7];
+  uint32_t red[2][4];
+  float factor[2];             // per staged row tile: 2^k scale log2(e)
+  alignas(16) float nlse[2][KT];   // -lse log2(e); -inf for rows that give no weight
+};
+constexpr int MASS_SMEM = 1024 + 2 * 2 * KSTAGE /*Q*/ + MK * KSTAGE + (int)sizeof(MassBars);
+static_assert(MASS_SMEM <= 232448, "shared memory budget");
+static_assert(MASS_SMEM > 233472 / 2, "tensor-memory kernels must not share an SM");
+
+__global__ void __launch_bounds__(NT, 1)
+attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ Params p, int q_rt) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = base;                          // [2][hi, lo]
+  uint8_t* sK = sQ + 4 * KSTAGE;               // [MK]
+  MassBars& bar = *reinterpret_cast<MassBars*>(sK + MK * KSTAGE);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Kv8AttnArgs& a = p.a;
+
+  if (tid == 0) {
+    bar.abort_flag = 0;
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bar.q_full[i], 4);
+      tc::mbar_init(&bar.q_empty[i], 1 + 8);
+    }
+    for (int i = 0; i < MK; ++i) {
+      tc::mbar_init(&bar.k_full[i], 1);
+      tc::mbar_init(&bar.k_empty[i], 1);
+    }
+    for (int i = 0; i < MS; ++i) {
+      tc::mbar_init(&bar.s_full[i], 1);
+      tc::mbar_init(&bar.s_empty[i], 4);
+    }
+    tc::mbar_init(&bar.done, 1);
+    tc::fence_mbar_init();
+    tc::prefetch_tmap(&tm_k);
+  }
+  if (warp == 1) tc::tmem_alloc(&bar.tmem_base, 512);
+  pdl_trigger();
+  if (warp == 0) {
+    pdl_wait();
+    make_walk(p, bar.walk);
+  }
+  __syncthreads();
+  pdl_wait();
+  volatile int* abort_flag = &bar.abort_flag;
+  const uint32_t tS = bar.tmem_base;
+  Walk w;
+  w.start(p, bar.walk);
+  auto arrive = [&](uint64_t* b) {       // once for the warp, after all its lanes
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(b);
+  };
+
+  if (warp == 0) {
+    if (tc::elect_one()) {
+      const uint64_t pol = q_rt > 1 ? tc::policy_evict_last() : tc::policy_evict_first();
+      uint32_t k = 0, ph = 1, filled = 0;
+      bool ok = true;
+      for (; w.n > 0 && ok; w.next(p)) {
+        const int bh = w.b * a.Hkv + w.h;
+        for (int rt = 0; rt < q_rt && ok; ++rt)
+          for (int t = w.ta; t < w.end(); ++t) {
+            if (!wait_bar(&bar.k_empty[k], ph, abort_flag, a.status, ST_TIMEOUT_PRODUCER)) { ok = false; break; }
+            tc::mbar_arrive_expect_tx(&bar.k_full[k], KSTAGE);
+            asm volatile(
+                "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+                " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(tc::smem_u32(sK + k * KSTAGE)),
+                "l"(reinterpret_cast<uint64_t>(&tm_k)), "r"(0), "r"(t * KT), "r"(bh),
+                "r"(tc::smem_u32(&bar.k_full[k])), "l"(pol)
+                : "memory");
+            ++filled;
+            if (++k == MK) {
+              k = 0;
+              ph ^= 1;
+            }
+          }
+      }
+      if (!ok)      // let the copies land before the CTA leaves
+        for (uint32_t i = filled > MK ? filled - MK : 0; i < filled; ++i)
+          tc::mbar_wait(&bar.k_full[i % MK], (i / MK) & 1, 1u << 12);
+    }
+  } else if (warp == 1) {
+    if (tc::elect_one()) {
+      const uint32_t id_s = (1u << 4) | ((KT >> 3) << 17) | ((KT >> 4) << 24);
+      const uint64_t dQ = tc::sdesc_k128(tc::smem_u32(sQ)), dK = tc::sdesc_k128(tc::smem_u32(sK));
+      uint32_t k = 0, kph = 0, sb = 0, sph = 1, seg = 0;
+      bool ok = true;
+      for (; w.n > 0 && ok; w.next(p))
+        for (int rt = 0; rt < q_rt && ok; ++rt, ++seg) {
+          const uint32_t qb = seg & 1;
+          const uint64_t dq = dQ + qb * (2 * KSTAGE >> 4);
+          if (!wait_bar(&bar.q_full[qb], (seg >> 1) & 1, abort_flag, a.status, ST_TIMEOUT_MMA)) { ok = false; break; }
+          for (int n = w.end() - w.ta; n > 0; --n) {
+            if (!wait_bar(&bar.s_empty[sb], sph, abort_flag, a.status, ST_TIMEOUT_MMA) ||
+                !wait_bar(&bar.k_full[k], kph, abort_flag, a.status, ST_TIMEOUT_MMA)) {
+              ok = false;
+              break;
+            }
+            tc::fence_after_sync();
+            const uint64_t dk = dK + k * (KSTAGE >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)      // hi, then lo
+              mma_f8(tS + sb * 128, dk + (kk & 3) * 2, dq + (kk >> 2) * (KSTAGE >> 4) + (kk & 3) * 2, id_s, kk != 0);
+            tc::mma_commit(&bar.s_full[sb]);
+            tc::mma_commit(&bar.k_empty[k]);
+            if (++k == MK) {
+              k = 0;
+              kph ^= 1;
+            }
+            if (++sb == MS) {
+              sb = 0;
+              sph ^= 1;
+            }
+          }
+          tc::mma_commit(&bar.q_empty[qb]);
+        }
+      tc::mma_commit(&bar.done);
+      tc::mbar_wait(&bar.done, 0, 1u << 20);
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------------ queries: four threads per row, 32 rows at a time
+    const int ct = tid - 384;
+    const uint32_t cw = warp - 12;
+    uint32_t seg = 0;
+    for (; w.n > 0; w.next(p))
+      for (int rt = 0; rt < q_rt; ++rt, ++seg) {
+        const uint32_t qb = seg & 1;
+        uint32_t m = 0;
+#pragma unroll 1
+        for (int r = ct >> 2; r < KT; r += 32) {
+          const __nv_bfloat16* src = query_row(p, w.b, w.h, rt, r);
+          Quarter q;
+          q.load(src ? src + 32 * (ct & 3) : nullptr);
+          const uint32_t x = q.amax();
+          m = max(m, x < kInfBits ? x : 0u);
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) bar.red[qb][cw] = m;
+        tc::named_bar_sync(kBarConv, 128);
+        const int k = bits_exp(max(max(bar.red[qb][0], bar.red[qb][1]), max(bar.red[qb][2], bar.red[qb][3])));
+        const float inv = kv8::exp2i(-k);
+        const int R = rt * KT + ct, qi = R / p.G;
+        float nl = -INFINITY;
+        if (R < p.n_rows) {
+          const float lse = a.lse_in[((int64_t)w.b * a.Lq + qi) * a.Hq + w.h * p.G + R - qi * p.G];
+          if (lse != -INFINITY) nl = -lse * kLog2e;
+        }
+        if (seg >= 2) wait_bar(&bar.q_empty[qb], ((seg >> 1) & 1) ^ 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+        bar.nlse[qb][ct] = nl;
+        if (ct == 0) bar.factor[qb] = kv8::exp2i(k) * (a.scale * kLog2e);
+#pragma unroll 1
+        for (int r = ct >> 2; r < KT; r += 32) {
+          const __nv_bfloat16* src = query_row(p, w.b, w.h, rt, r);
+          Quarter q;
+          q.load(src ? src + 32 * (ct & 3) : nullptr);
+          // an infinity or NaN in a row makes its codes NaN, and with them its weight on every key
+          q.split(q.amax() < kInfBits ? inv : qnan(), r, ct & 3, sQ + qb * 2 * KSTAGE, sQ + (qb * 2 + 1) * KSTAGE);
+        }
+        fence_async_smem();
+        arrive(&bar.q_full[qb]);
+      }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ weights
+    const int grp = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const int64_t runs = (a.cap + a.S - 1) / a.S;
+    uint32_t it = 0, sb = 0, ph = 0, seg = 0;
+    for (; w.n > 0; w.next(p)) {
+      const int64_t bh = (int64_t)w.b * a.Hkv + w.h;
+      const int t_end = w.end();
+      for (int rt = 0; rt < q_rt; ++rt, ++seg) {
+        const uint32_t qb = seg & 1;
+        const int cols = min(KT, p.n_rows - rt * KT);
+        wait_bar(&bar.q_full[qb], (seg >> 1) & 1, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+        const float f = bar.factor[qb];
+        // the other group may have added the last row tile to this group's tiles
+        if (rt > 0) tc::named_bar_sync(kBarPair, 256);
+        for (int t = w.ta; t < t_end; ++t, ++it) {
+          if ((int)(it & 1) == grp) {
+            const int key = t * KT + row;
+            const bool live = key < w.len;
+            float ks = 0.f, old = 0.f;
+            const int64_t at = bh * a.cap + key;
+            if (live) {
+              ks = a.k_scale[bh * runs + key / a.S];
+              if (rt > 0) old = a.mass_out[at];
+              else if (a.mass_in) old = a.decay * a.mass_in[at];
+            }
+            wait_bar(&bar.s_full[sb], ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+            __syncwarp();
+            tc::fence_after_sync();
+            const float c = f * ks;
+            const uint64_t c2 = pk2(c, c);
+            uint64_t s2 = pk2(0.f, 0.f);
+#pragma unroll 1
+            for (int j = 0; j < cols; j += 32) {
+              float v[32];
+              tmem_ld32(tS + sb * 128 + j + lane_off, v);
+              const float4* nl = reinterpret_cast<const float4*>(bar.nlse[qb] + j);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 n4 = nl[i];
+                float x0, x1, x2, x3;
+                upk2(fma2(pk2(v[4 * i], v[4 * i + 1]), c2, pk2(n4.x, n4.y)), x0, x1);
+                upk2(fma2(pk2(v[4 * i + 2], v[4 * i + 3]), c2, pk2(n4.z, n4.w)), x2, x3);
+                s2 = add2(s2, pk2(ex2(x0), ex2(x1)));
+                s2 = add2(s2, pk2(ex2(x2), ex2(x3)));
+              }
+            }
+            tc::fence_before_sync();
+            arrive(&bar.s_empty[sb]);
+            float s0, s1;
+            upk2(s2, s0, s1);
+            if (live && !*abort_flag) a.mass_out[at] = old + (s0 + s1);
+          }
+          if (++sb == MS) {
+            sb = 0;
+            ph ^= 1;
+          }
+        }
+        arrive(&bar.q_empty[qb]);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(bar.tmem_base, 512);
+  }
+}
+
 int encode_codes(CUtensorMap* m, const void* codes, int64_t cap, int64_t bh) {
   EncodeTiledFn enc = encoder();
   if (!enc) {
@@ -979,6 +1227,25 @@ int launch_attn_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
     launch_pdl(attn_kv8_merge_kernel, (unsigned)((int64_t)a.B * a.Hkv * p.n_rt * (128 / kMergeCols)), KT, 0, s, p);
     DLLM_CHECK_LAUNCH("attn_kv8_merge_kernel");
   }
+  return DLLM_OK;
+}
+
+int launch_attn_mass_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
+  Params p = {};
+  p.a = a;
+  p.a.k_own = nullptr;
+  p.G = a.Hq / a.Hkv;
+  p.n_rows = a.Lq * p.G;
+  p.n_rt = 1;                  // units of the walk are whole (b, kv head)s
+  const int64_t most = (int64_t)a.B * a.Hkv * ((a.P + KT - 1) / KT);
+  p.n_cta = (int)std::min<int64_t>(num_sms(), most);
+  CUtensorMap mk;
+  int st = encode_codes(&mk, a.k_codes, a.cap, (int64_t)a.B * a.Hkv);
+  if (st) return st;
+  st = set_max_smem<attn_mass_kv8_tc_kernel>(MASS_SMEM);
+  if (st) return st;
+  launch_pdl(attn_mass_kv8_tc_kernel, p.n_cta, NT, MASS_SMEM, s, mk, p, (p.n_rows + KT - 1) / KT);
+  DLLM_CHECK_LAUNCH("attn_mass_kv8_tc_kernel");
   return DLLM_OK;
 }
 

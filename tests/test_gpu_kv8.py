@@ -263,7 +263,9 @@ def test_block_attn_kv8_nan_queries_stay_their_own(dtype, d):
 MASS = [("f32", 2, 5, 6, 2, 80, 100, 32, (1, 99)), ("f32", 1, 33, 3, 1, 16, 70, 16, None),
         ("bf16", 1, 32, 16, 4, 128, 300, 32, None), ("bf16", 3, 1, 28, 4, 128, 515, 16, (515, 0, 129)),
         ("bf16", 2, 40, 16, 2, 128, 260, 64, (257, 128)), ("bf16", 1, 300, 5, 1, 128, 150, 128, (149,)),
-        ("bf16", 20, 3, 4, 4, 128, 140, 16, tuple(range(121, 141)))]
+        ("bf16", 20, 3, 4, 4, 128, 140, 16, tuple(range(121, 141))),
+        ("bf16", 40, 70, 8, 2, 128, 700, 64, tuple(i * 17 % 701 for i in range(40))),   # several row and key tiles a CTA
+        ("bf16", 1, 1, 2, 2, 128, 1, 16, None)]
 
 
 @pytest.mark.parametrize("dtype,B,Lq,Hq,Hkv,d,P,S,lens", MASS)
