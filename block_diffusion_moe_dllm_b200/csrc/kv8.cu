@@ -8,6 +8,7 @@
 #include "kv8.cuh"
 #include "kv8.h"
 #include "misc.h"
+#include <algorithm>
 
 namespace dllm {
 namespace {
@@ -109,87 +110,146 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
 // negative values count as 0), above every weight for the positions that are always kept.
 constexpr uint32_t kForced = 0x7f800001u;
 
-// One CTA per selection (batch row, or batch row and kv head): keys, the n_keep-th largest key by a radix search
-// over bytes, then the kept positions in increasing order (equal keys at the threshold: the lower position first).
-__global__ void __launch_bounds__(1024) kv8_select_kernel(const Kv8EvictArgs a, uint32_t* __restrict__ keys,
-                                                          int32_t* __restrict__ index) {
+// One cluster per selection (batch row, or batch row and kv head), each of its C CTAs on a contiguous part of the
+// positions: the n_keep-th largest key by a radix search over digits of 11, 11 and 10 bits (histograms added up through
+// distributed shared memory; 11 bits spread the exponents of a heavy-tailed accumulator over enough counters that the
+// shared-memory atomics hardly collide), then the kept positions in increasing order (equal keys at the threshold: the
+// lower position first). Keys stay in shared memory where the part fits, else in the workspace.
+constexpr int kSelThreads = 1024, kBins = 2048;
+constexpr int kSelPart = 2048;              // positions for which a selection gets another CTA
+constexpr int kSelSmemKeys = 32768;         // keys of a part that fit shared memory
+
+DLLM_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+DLLM_DEV uint32_t peer_u32(const void* mine, uint32_t rank) {    // the same shared variable of another CTA of the cluster
+  uint32_t v, at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kSelThreads, 1) kv8_select_kernel(const Kv8EvictArgs a, int C, uint32_t* __restrict__ keys,
+                                                                    int32_t* __restrict__ index) {
   pdl_enter();
-  __shared__ unsigned hist[256];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
-  __shared__ int wsum[32];
-  const int sel = blockIdx.x, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  extern __shared__ uint32_t dyn[];
+  __shared__ uint32_t hist[2][kBins];
+  __shared__ uint32_t wsum[32], wsum2[32];
+  __shared__ uint32_t s_bin, s_need;
+  __shared__ uint32_t counts[2];             // of this part: keys above the threshold, keys equal to it
+  const int rank = blockIdx.x % C, sel = blockIdx.x / C;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int Hs = a.per_head ? a.Hkv : 1;
   const int b = sel / Hs, h = sel - b * Hs;
   const int len = kv8::prefix_len(a.lens, b, a.P);
   const int keep = min(len, a.n_keep);
-  uint32_t* key = keys + (int64_t)sel * a.P;
-  if (h == 0 && tid == 0) a.len_out[b] = keep;
-  for (int j = tid; j < len; j += 1024) {
+  const int part = (len + C - 1) / C, lo = min(len, rank * part), n = min(len, lo + part) - lo;
+  uint32_t* key = (a.P + C - 1) / C <= kSelSmemKeys ? dyn : keys + (int64_t)sel * a.P + lo;
+  if (h == 0 && rank == 0 && tid == 0) a.len_out[b] = keep;
+  const float* m = a.mass + (int64_t)b * a.Hkv * a.cap;
+  for (int i = tid; i < n; i += kSelThreads) {
+    const int j = lo + i;
     // the heads' weights are summed in 64 bits, in head order
     double t = 0.0;
     if (a.per_head) {
-      t = a.mass[((int64_t)b * a.Hkv + h) * a.cap + j];
+      t = m[(int64_t)h * a.cap + j];
     } else {
-      for (int g = 0; g < a.Hkv; ++g) t += (double)a.mass[((int64_t)b * a.Hkv + g) * a.cap + j];
+#pragma unroll 4
+      for (int g = 0; g < a.Hkv; ++g) t += (double)m[(int64_t)g * a.cap + j];
     }
     const float f = (float)t;
-    key[j] = (j < a.n_first || j >= len - a.n_last) ? kForced : __float_as_uint(f > 0.f ? f : 0.f);
+    key[i] = (j < a.n_first || j >= len - a.n_last) ? kForced : __float_as_uint(f > 0.f ? f : 0.f);
   }
   uint32_t prefix = 0, mask = 0;
-  int need = keep;      // how many of the keys that match the prefix are still to be taken
-  __syncthreads();
-  for (int shift = 24; shift >= 0 && keep > 0 && keep < len; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
+  uint32_t need = (uint32_t)keep;      // how many of the keys that match the prefix are still to be taken
+  const bool all = keep == len;        // the whole cluster agrees
+  for (int pass = 0; pass < 3 && !all; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    uint32_t* hs = hist[pass & 1];
+    hs[tid] = hs[tid + kSelThreads] = 0;
     __syncthreads();
-    for (int j = tid; j < len; j += 1024) {
-      const uint32_t u = key[j];
-      if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1u);
+    for (int i = tid; i < n; i += kSelThreads) {
+      const uint32_t u = key[i];
+      if ((u & mask) == prefix) atomicAdd(&hs[(u >> shift) & ((1u << bits) - 1u)], 1u);
+    }
+    cluster_sync();
+    // thread t holds bins 2047 - 2 t and 2046 - 2 t: a prefix sum over the threads counts from the largest key down
+    uint32_t c0 = 0, c1 = 0;
+    for (int r = 0; r < C; ++r) {
+      c0 += peer_u32(&hs[kBins - 1 - 2 * tid], r);
+      c1 += peer_u32(&hs[kBins - 2 - 2 * tid], r);
+    }
+    uint32_t run = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
+    }
+    if (lane == 31) wsum[w] = run;
+    __syncthreads();
+    uint32_t above = run - (c0 + c1);
+    for (int i = 0; i < 32; ++i) above += i < w ? wsum[i] : 0u;
+    if (above < need && need <= above + c0 + c1) {      // exactly one thread of the CTA
+      const bool first = need <= above + c0;
+      s_bin = (uint32_t)(kBins - 1 - 2 * tid) - (first ? 0u : 1u);
+      s_need = need - above - (first ? 0u : c0);
     }
     __syncthreads();
-    if (tid == 0) {
-      int left = need, bin = 255;
-      while (bin > 0 && (int)hist[bin] < left) left -= (int)hist[bin--];
-      s_need = left;
-      s_prefix = prefix | ((uint32_t)bin << shift);
-    }
-    __syncthreads();
-    prefix = s_prefix;
+    prefix |= s_bin << shift;
     need = s_need;
-    mask |= 255u << shift;
+    mask |= ((1u << bits) - 1u) << shift;
   }
-  // prefix is now the threshold: larger keys are kept, and the first `need` equal ones
-  const bool all = keep == len;
-  int base = 0, base_eq = 0;
-  const int32_t* pos = a.pos ? a.pos + (int64_t)sel * a.cap : nullptr;
-  for (int j0 = 0; j0 < len; j0 += 1024) {
-    const int j = j0 + tid;
-    const uint32_t u = j < len ? key[j] : 0u;
-    const bool eq = j < len && !all && u == prefix;
-    bool take = j < len && (all || u > prefix);
-    // rank among the equal keys, then rank among the kept positions
-    for (int pass = 0; pass < 2; ++pass) {
-      const unsigned bal = __ballot_sync(0xffffffffu, pass == 0 ? eq : take);
-      __syncthreads();
-      if (lane == 0) wsum[w] = __popc(bal);
-      __syncthreads();
-      int before = 0, total = 0;
-      for (int k = 0; k < 32; ++k) {
-        before += k < w ? wsum[k] : 0;
-        total += wsum[k];
-      }
-      const int rank = before + __popc(bal & ((1u << lane) - 1u));
-      if (pass == 0) {
-        take |= eq && base_eq + rank < need;
-        base_eq += total;
-      } else {
-        if (take) {
-          index[(int64_t)sel * a.n_keep + base + rank] = j;
-          a.keep_pos[(int64_t)sel * a.cap_out + base + rank] = pos ? pos[j] : j;
-        }
-        base += total;
-      }
+  // prefix is now the threshold: larger keys are kept, and the first `need` equal ones. Each warp takes a contiguous
+  // stretch of the part: it counts, the counts are summed over warps and CTAs, and it writes.
+  const int per_warp = (n + 31) / 32, w0 = min(n, w * per_warp), w1 = min(n, w0 + per_warp);
+  uint32_t gt = 0, eq = 0;
+  __syncthreads();
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t u = i < w1 ? key[i] : 0u;
+    gt += __popc(__ballot_sync(0xffffffffu, i < w1 && (all || u > prefix)));
+    eq += __popc(__ballot_sync(0xffffffffu, i < w1 && !all && u == prefix));
+  }
+  if (lane == 0) {
+    wsum[w] = gt;
+    wsum2[w] = eq;
+  }
+  __syncthreads();
+  uint32_t gt_before = 0, eq_before = 0, gt_all = 0, eq_all = 0;
+  for (int i = 0; i < 32; ++i) {
+    gt_before += i < w ? wsum[i] : 0u;
+    eq_before += i < w ? wsum2[i] : 0u;
+    gt_all += wsum[i];
+    eq_all += wsum2[i];
+  }
+  if (tid == 0) {
+    counts[0] = gt_all;
+    counts[1] = eq_all;
+  }
+  cluster_sync();
+  for (int r = 0; r < rank; ++r) {
+    gt_before += peer_u32(&counts[0], r);
+    eq_before += peer_u32(&counts[1], r);
+  }
+  cluster_sync();        // no CTA leaves while another reads its counts
+  const int32_t* pos = a.pos ? a.pos + (int64_t)sel * a.cap + lo : nullptr;
+  int32_t* out = a.keep_pos + (int64_t)sel * a.cap_out;
+  int32_t* idx = index + (int64_t)sel * a.n_keep;
+  const unsigned below = (1u << lane) - 1u;
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t u = i < w1 ? key[i] : 0u;
+    const unsigned g = __ballot_sync(0xffffffffu, i < w1 && (all || u > prefix));
+    const unsigned e = __ballot_sync(0xffffffffu, i < w1 && !all && u == prefix);
+    const uint32_t eq_rank = eq_before + __popc(e & below);
+    const bool take = (g >> lane & 1u) || ((e >> lane & 1u) && eq_rank < need);
+    if (take) {
+      const uint32_t at = gt_before + __popc(g & below) + min(eq_rank, need);
+      idx[at] = lo + i;
+      out[at] = pos ? pos[i] : lo + i;
     }
+    gt_before += __popc(g);
+    eq_before += __popc(e);
   }
 }
 
@@ -284,7 +344,30 @@ int launch_kv8_evict(const Kv8EvictArgs& a, cudaStream_t s) {
   const int64_t sel = (int64_t)a.B * (a.per_head ? a.Hkv : 1);
   uint32_t* keys = static_cast<uint32_t*>(a.ws);
   int32_t* index = reinterpret_cast<int32_t*>(static_cast<char*>(a.ws) + ((size_t)sel * a.P * 4 + 255) / 256 * 256);
-  launch_pdl(kv8_select_kernel, (unsigned)sel, 1024, 0, s, a, keys, index);
+  {
+    // CTAs of a selection: enough that a thread handles few positions, at most a portable cluster
+    const int C = std::min(8, std::max(1, (a.P + kSelPart - 1) / kSelPart));
+    const int part = (a.P + C - 1) / C;
+    const size_t smem = part <= kSelSmemKeys ? (size_t)part * 4 : 0;
+    const int st = set_max_smem<kv8_select_kernel>(kSelSmemKeys * 4);
+    if (st) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sel * C), 1, 1);
+    cfg.blockDim = dim3(kSelThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_select_kernel, a, C, keys, index);
+    if (e != cudaSuccess) return dllm_host::cuda_status(e, "cudaLaunchKernelEx(kv8_select_kernel)");
+  }
   DLLM_CHECK_LAUNCH("kv8_select_kernel");
   const int most = min(a.n_keep, a.P);
   if (most == 0) return DLLM_OK;

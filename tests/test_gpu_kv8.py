@@ -301,7 +301,9 @@ def test_attn_mass_kv8(dtype, B, Lq, Hq, Hkv, d, P, S, lens, start):
 EVICT = [(1, 1, 128, 1, 16, 1, 0, 0, None), (2, 4, 128, 300, 32, 150, 4, 64, (300, 171)),
          (3, 2, 64, 257, 16, 100, 0, 0, (257, 0, 99)), (2, 3, 128, 1500, 64, 1400, 1, 1, (1500, 1401)),
          (1, 2, 32, 5000, 128, 333, 8, 100, (4999,)), (2, 2, 128, 90, 32, 200, 2, 2, (90, 1)),
-         (1, 1, 16, 2100, 16, 64, 64, 0, None), (2, 1, 128, 40, 128, 39, 0, 39, (40, 38))]
+         (1, 1, 16, 2100, 16, 64, 64, 0, None), (1, 2, 16, 20001, 64, 7000, 3, 5, (19999,)),
+         (1, 1, 16, 270000, 128, 30000, 0, 0, None),     # keys in the workspace
+         (2, 1, 128, 40, 128, 39, 0, 39, (40, 38))]
 
 
 @pytest.mark.parametrize("B,Hkv,d,P,S,keep,first,last,lens", EVICT)
