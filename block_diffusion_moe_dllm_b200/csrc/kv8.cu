@@ -39,7 +39,6 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
   const int nvec = ok ? rows * vpr : 0;
   const T* src = static_cast<const T*>(is_v ? a.v : a.k) + bh * (int64_t)a.cap_src * a.d;
   uint4 vec[VPT];
-  float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int id = gt + i * TG;
@@ -51,22 +50,33 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
       if (row >= 0 && row < a.cap_src) vec[i] = ld_nc_v4(src + (int64_t)row * a.d + (int64_t)c * VE);
     }
   }
-  auto values = [&](const uint4& u, float* f) {
-    if constexpr (sizeof(T) == 2) {
-      bf16x8_to_f32(u, f);
-    } else {
-      f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-      f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
-    }
-  };
+  // Magnitudes compare as their bits. Infinities and NaN, which do not count (infinities saturate, NaN stays NaN), show as
+  // the largest patterns; the values are then looked at one by one.
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    float f[VE];
-    values(vec[i], f);
-#pragma unroll
-    for (int j = 0; j < VE; ++j) {
-      const float m = fabsf(f[j]);
-      if (m < INFINITY) amax = fmaxf(amax, m);     // infinities saturate, NaN stays NaN
+    const uint4& u = vec[i];
+    if constexpr (sizeof(T) == 2) {
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                   __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+    } else {
+      top = max(top, max(max(u.x & 0x7fffffffu, u.y & 0x7fffffffu), max(u.z & 0x7fffffffu, u.w & 0x7fffffffu)));
+    }
+  }
+  if constexpr (sizeof(T) == 2) top = max(top & 0xffffu, top >> 16) << 16;
+  float amax = __uint_as_float(top);
+  if (top >= 0x7f800000u) {
+    amax = 0.f;
+#pragma unroll 1
+    for (int id = gt; id < nvec; id += TG) {
+      const int r = id / vpr, c = id - r * vpr;
+      int row = a.src_row + t0 + r;
+      if (a.src_pos) row = a.src_pos[(int64_t)b * a.pos_stride + t0 + r];
+      if (row < 0 || row >= a.cap_src) continue;
+      for (int j = 0; j < VE; ++j) {
+        const float m = fabsf(to_f32(src[(int64_t)row * a.d + c * VE + j]));
+        if (m < INFINITY) amax = fmaxf(amax, m);
+      }
     }
   }
   amax = warp_max(amax);
@@ -85,13 +95,22 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
   for (int i = 0; i < VPT; ++i) {
     const int id = gt + i * TG;
     if (id < nvec) {
-      float f[VE];
-      values(vec[i], f);
+      const uint32_t u[4] = {vec[i].x, vec[i].y, vec[i].z, vec[i].w};
       uint32_t w[VE / 4];
 #pragma unroll
-      for (int j = 0; j < VE / 4; ++j)
-        w[j] = kv8::f32x2_to_e4m3x2(f[4 * j] * inv, f[4 * j + 1] * inv) |
-               (kv8::f32x2_to_e4m3x2(f[4 * j + 2] * inv, f[4 * j + 3] * inv) << 16);
+      for (int j = 0; j < VE / 4; ++j) {
+        float f[4];
+        if constexpr (sizeof(T) == 2) {
+          f[0] = __uint_as_float(u[2 * j] << 16);
+          f[1] = __uint_as_float(u[2 * j] & 0xffff0000u);
+          f[2] = __uint_as_float(u[2 * j + 1] << 16);
+          f[3] = __uint_as_float(u[2 * j + 1] & 0xffff0000u);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(u[k]);
+        }
+        w[j] = kv8::f32x2_to_e4m3x2(f[0] * inv, f[1] * inv) | (kv8::f32x2_to_e4m3x2(f[2] * inv, f[3] * inv) << 16);
+      }
       // the run's rows are contiguous, so vector id of the source lands at id * VE codes
       if constexpr (VE == 8)
         *reinterpret_cast<uint2*>(dst + (int64_t)id * 8) = make_uint2(w[0], w[1]);
@@ -116,7 +135,7 @@ constexpr uint32_t kForced = 0x7f800001u;
 // shared-memory atomics hardly collide), then the kept positions in increasing order (equal keys at the threshold: the
 // lower position first). Keys stay in shared memory where the part fits, else in the workspace.
 constexpr int kSelThreads = 1024, kBins = 2048;
-constexpr int kSelPart = 2048;              // positions for which a selection gets another CTA
+constexpr int kSelPart = 4096;              // positions for which a selection gets another CTA
 constexpr int kSelSmemKeys = 32768;         // keys of a part that fit shared memory
 
 DLLM_DEV void cluster_sync() {
@@ -129,11 +148,17 @@ DLLM_DEV uint32_t peer_u32(const void* mine, uint32_t rank) {    // the same sha
   return v;
 }
 
+DLLM_DEV void peer_store_u32(void* mine, uint32_t rank, uint32_t v) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
 __global__ void __launch_bounds__(kSelThreads, 1) kv8_select_kernel(const Kv8EvictArgs a, int C, uint32_t* __restrict__ keys,
                                                                     int32_t* __restrict__ index) {
   pdl_enter();
   extern __shared__ uint32_t dyn[];
-  __shared__ uint32_t hist[2][kBins];
+  __shared__ uint32_t hist[2][kBins], sums[kBins];
   __shared__ uint32_t wsum[32], wsum2[32];
   __shared__ uint32_t s_bin, s_need;
   __shared__ uint32_t counts[2];             // of this part: keys above the threshold, keys equal to it
@@ -147,18 +172,28 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv8_select_kernel(const Kv8Evi
   uint32_t* key = (a.P + C - 1) / C <= kSelSmemKeys ? dyn : keys + (int64_t)sel * a.P + lo;
   if (h == 0 && rank == 0 && tid == 0) a.len_out[b] = keep;
   const float* m = a.mass + (int64_t)b * a.Hkv * a.cap;
-  for (int i = tid; i < n; i += kSelThreads) {
-    const int j = lo + i;
-    // the heads' weights are summed in 64 bits, in head order
-    double t = 0.0;
-    if (a.per_head) {
-      t = m[(int64_t)h * a.cap + j];
-    } else {
-#pragma unroll 4
-      for (int g = 0; g < a.Hkv; ++g) t += (double)m[(int64_t)g * a.cap + j];
+  // kFlight positions of a thread are loaded before the first is used
+  constexpr int kFlight = 8;
+  const int heads = a.per_head ? 1 : a.Hkv;
+  if (a.per_head) m += (int64_t)h * a.cap;
+  for (int i0 = tid; i0 < n; i0 += kFlight * kSelThreads) {
+    double t[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) t[k] = 0.0;
+    for (int g = 0; g < heads; ++g) {        // summed in 64 bits, in head order
+      float f[kFlight];
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k)
+        f[k] = i0 + k * kSelThreads < n ? m[(int64_t)g * a.cap + lo + i0 + k * kSelThreads] : 0.f;
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) t[k] += (double)f[k];
     }
-    const float f = (float)t;
-    key[i] = (j < a.n_first || j >= len - a.n_last) ? kForced : __float_as_uint(f > 0.f ? f : 0.f);
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int i = i0 + k * kSelThreads, j = lo + i;
+      const float f = (float)t[k];
+      if (i < n) key[i] = (j < a.n_first || j >= len - a.n_last) ? kForced : __float_as_uint(f > 0.f ? f : 0.f);
+    }
   }
   uint32_t prefix = 0, mask = 0;
   uint32_t need = (uint32_t)keep;      // how many of the keys that match the prefix are still to be taken
@@ -168,17 +203,25 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv8_select_kernel(const Kv8Evi
     uint32_t* hs = hist[pass & 1];
     hs[tid] = hs[tid + kSelThreads] = 0;
     __syncthreads();
+#pragma unroll 4
     for (int i = tid; i < n; i += kSelThreads) {
       const uint32_t u = key[i];
       if ((u & mask) == prefix) atomicAdd(&hs[(u >> shift) & ((1u << bits) - 1u)], 1u);
     }
     cluster_sync();
-    // thread t holds bins 2047 - 2 t and 2046 - 2 t: a prefix sum over the threads counts from the largest key down
-    uint32_t c0 = 0, c1 = 0;
-    for (int r = 0; r < C; ++r) {
-      c0 += peer_u32(&hs[kBins - 1 - 2 * tid], r);
-      c1 += peer_u32(&hs[kBins - 2 - 2 * tid], r);
+    if (C > 1) {      // each CTA adds up its share of the bins over the cluster and gives every CTA the sums
+      const int per = kBins / C;
+      for (int i = tid; i < per; i += kSelThreads) {
+        const int bin = rank * per + i;
+        uint32_t t = 0;
+        for (int r = 0; r < C; ++r) t += peer_u32(&hs[bin], r);
+        for (int r = 0; r < C; ++r) peer_store_u32(&sums[bin], r, t);
+      }
+      cluster_sync();
     }
+    // thread t holds bins 2047 - 2 t and 2046 - 2 t: a prefix sum over the threads counts from the largest key down
+    const uint32_t* tot = C > 1 ? sums : hs;
+    const uint32_t c0 = tot[kBins - 1 - 2 * tid], c1 = tot[kBins - 2 - 2 * tid];
     uint32_t run = c0 + c1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -283,26 +326,40 @@ __global__ void __launch_bounds__(kThreads) kv8_gather_kernel(const Kv8EvictArgs
   }
   __syncthreads();
   if (rows <= 0) return;
+  // S d / 16 vectors of K and as many of V, at most 4 of each per thread (d <= 128), all loaded before the first is used
   const int vpr = a.d / 16, nvec = rows * vpr;
+  uint4 vec[2][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int id = gt + i * TG;
+    if (id < nvec) {
+      const int r = id / vpr;
+      const int64_t at = bh * (int64_t)a.cap * a.d + (int64_t)src_s[grp][r] * a.d + (id - r * vpr) * 16;
+      vec[0][i] = ld_nc_v4(a.k_codes + at);
+      vec[1][i] = ld_nc_v4(a.v_codes + at);
+    }
+  }
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
     float top = 0.f;
-    for (int r = 0; r < rows; ++r) top = fmaxf(top, sc_s[grp][kv][r]);
-    const uint8_t* src = (kv ? a.v_codes : a.k_codes) + bh * (int64_t)a.cap * a.d;
+#pragma unroll
+    for (int r = 0; r < S; ++r) top = fmaxf(top, r < rows ? sc_s[grp][kv][r] : 0.f);
     uint8_t* dst = (kv ? a.v_out : a.k_out) + (bh * (int64_t)a.cap_out + t0) * a.d;
-    for (int id = gt; id < nvec; id += TG) {
-      const int r = id / vpr, c = id - r * vpr;
-      uint4 u = ld_nc_v4(src + (int64_t)src_s[grp][r] * a.d + c * 16);
-      const float old = sc_s[grp][kv][r];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int id = gt + i * TG;
+      if (id >= nvec) break;
+      uint4 u = vec[kv][i];
+      const float old = sc_s[grp][kv][id / vpr];
       if (old != top) {
         const float ratio = top > 0.f ? old / top : 0.f;
         float f[16];
         kv8::codes16_to_f32(u, f);
         uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o[i] = kv8::f32x2_to_e4m3x2(f[4 * i] * ratio, f[4 * i + 1] * ratio) |
-                 (kv8::f32x2_to_e4m3x2(f[4 * i + 2] * ratio, f[4 * i + 3] * ratio) << 16);
+        for (int j = 0; j < 4; ++j)
+          o[j] = kv8::f32x2_to_e4m3x2(f[4 * j] * ratio, f[4 * j + 1] * ratio) |
+                 (kv8::f32x2_to_e4m3x2(f[4 * j + 2] * ratio, f[4 * j + 3] * ratio) << 16);
         u = make_uint4(o[0], o[1], o[2], o[3]);
       }
       *reinterpret_cast<uint4*>(dst + (int64_t)id * 16) = u;
@@ -346,7 +403,8 @@ int launch_kv8_evict(const Kv8EvictArgs& a, cudaStream_t s) {
   int32_t* index = reinterpret_cast<int32_t*>(static_cast<char*>(a.ws) + ((size_t)sel * a.P * 4 + 255) / 256 * 256);
   {
     // CTAs of a selection: enough that a thread handles few positions, at most a portable cluster
-    const int C = std::min(8, std::max(1, (a.P + kSelPart - 1) / kSelPart));
+    int C = 1;
+    while (C < 8 && C * kSelPart < a.P) C *= 2;
     const int part = (a.P + C - 1) / C;
     const size_t smem = part <= kSelSmemKeys ? (size_t)part * 4 : 0;
     const int st = set_max_smem<kv8_select_kernel>(kSelSmemKeys * 4);
