@@ -293,10 +293,11 @@ def _device_stream(t, stream):
     """The stream's handle, after checking that the call's tensors are on the current device (the library launches
     there)."""
     import torch
-    if t.get_device() != torch.cuda.current_device():
-        raise DllmError(ERR_INVALID_ARG, f"tensors on device {t.get_device()}, current device "
-                                         f"{torch.cuda.current_device()}")
-    return stream_handle(stream)
+    dev, current = t.get_device(), torch.cuda.current_device()
+    if dev != current:
+        raise DllmError(ERR_INVALID_ARG, f"tensors on device {dev}, current device {current}")
+    # the handle alone: building the Stream object of the current stream takes 3 us of a 10 us call
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(current)
 
 
 def kv8_store(k, v, k_codes, v_codes, k_scale, v_scale, B, Hkv, d, n, cap_src, cap, scale_len, dtype, src_row=0,

@@ -58,6 +58,44 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kBarConv = 1, kBarPair = 2;
 constexpr int kPart = 33 * 128 * 4;        // floats of one partial result: 32 float4 columns and (m, l, -, -), by row
 
+// Code size is speed here: four kinds of warps run different loops on every scheduler, and what does not fit the
+// instruction caches is fetched again for every tile. Waits are therefore written compactly (the reason for giving up is
+// left in the abort flag and reported once, at the end), divisions are multiplications, and every loop body appears once.
+DLLM_DEV bool wait_for(uint64_t* bar, uint32_t parity, int* abort_flag, int code) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u32 n, f;\n\t"
+      "mov.u32 n, 0;\n\t"
+      "WAIT_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mov.u32 %0, 1;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "ld.volatile.shared.u32 f, [%3];\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "setp.ne.u32 p, f, 0;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 p, n, 4194304;\n\t"
+      "@p bra WAIT_%=;\n\t"
+      "st.volatile.shared.u32 [%3], %4;\n\t"
+      "DONE_%=:\n\t}"
+      : "=&r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity), "r"(tc::smem_u32(abort_flag)), "r"(code)
+      : "memory");
+  return ok != 0;
+}
+
+// n / d for 0 <= n < 2^31 (n * m >> shift; see attn_tc.cu).
+struct FastDiv {
+  uint32_t m, shift;
+  DLLM_DEV int operator()(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> shift); }
+};
+FastDiv fast_div(int d) {
+  uint32_t sh = 0;
+  while ((1u << sh) < (uint32_t)d) ++sh;
+  return {(uint32_t)((((uint64_t)1 << (31 + sh)) + (uint64_t)d - 1) / (uint64_t)d), 31 + sh};
+}
+
 struct Bars {
   uint64_t q_full, q_empty;
   uint64_t k_full[NK], k_empty[NK];
@@ -85,6 +123,8 @@ static_assert(SMEM > 233472 / 2, "tensor-memory kernels must not share an SM");
 struct Params {
   Kv8AttnArgs a;
   int G, n_rows, n_rt;        // rows Lq * G of a (b, kv head), row tiles
+  FastDiv by_G, by_blk;
+  int s_shift;                // log2 of scale_len
   int64_t own_sum;            // own key tiles of all row tiles of a (b, kv head)
   int n_cta;
   float* part;                // [n_cta][2][kPart]
@@ -92,11 +132,12 @@ struct Params {
   int reuse;                  // several row tiles read the same keys: keep them in L2
 };
 
+// Own keys that query q sees: up to the end of its block. (blk_len is at most Lq here, see the launch.)
+DLLM_DEV int visible_own(const Params& p, int q) { return min(p.a.Lq, (p.by_blk(q) + 1) * p.a.blk_len); }
 // Own keys that rows of tile rt see (their last query's block).
 DLLM_DEV int own_keys(const Params& p, int rt) {
   if (!p.a.k_own) return 0;
-  const int last_q = (min((rt + 1) * KT, p.n_rows) - 1) / p.G;
-  return (int)min((int64_t)p.a.Lq, ((int64_t)(last_q / p.a.blk_len) + 1) * p.a.blk_len);
+  return visible_own(p, p.by_G(min((rt + 1) * KT, p.n_rows) - 1));
 }
 DLLM_DEV int cdiv128(int x) { return (int)(((unsigned)x + 127u) >> 7); }
 // Key tiles of all units of batch row b: at least one per unit, so that rows without keys are written too. The host
@@ -264,7 +305,7 @@ DLLM_DEV float qnan() { return __int_as_float(0x7fffffff); }
 DLLM_DEV int bits_exp(uint32_t bf16_bits) { return kv8::scale_exp(__uint_as_float(bf16_bits << 16)); }
 // Address of a unit's query row (NULL past the last).
 DLLM_DEV const __nv_bfloat16* query_row(const Params& p, int b, int h, int rt, int r) {
-  const int R = rt * KT + r, qi = R / p.G;
+  const int R = rt * KT + r, qi = p.by_G(R);
   return R < p.n_rows ? static_cast<const __nv_bfloat16*>(p.a.q) +
                             (((int64_t)b * p.a.Lq + qi) * p.a.Hq + h * p.G + R - qi * p.G) * 128
                       : nullptr;
@@ -428,13 +469,13 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             // own rows: the converters write two K stages (V goes past the code ring). This thread alone waits for
             // free stages, in order, and hands them over: waiting for one's own slots only would miss whole phases
             for (int i = t < w.tp + cdiv128(w.own) ? 2 : 1; i > 0 && ok; --i, ++ks) {
-              ok = wait_bar(&bar.k_empty[ks % NK], ((ks / NK) & 1) ^ 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+              ok = wait_for(&bar.k_empty[ks % NK], ((ks / NK) & 1) ^ 1, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
               if (ok) tc::mbar_arrive(&bar.k_grant[ks % NK]);
             }
             continue;
           }
           const uint32_t k = ks % NK, v = vs % NV;
-          if (!wait_bar(&bar.k_empty[k], ((ks / NK) & 1) ^ 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER)) { ok = false; break; }
+          if (!wait_for(&bar.k_empty[k], ((ks / NK) & 1) ^ 1, &bar.abort_flag, ST_TIMEOUT_PRODUCER)) { ok = false; break; }
           tc::mbar_arrive_expect_tx(&bar.k_full[k], KSTAGE);
           // rows past the cache read as zeros, rows past the prefix are masked
           asm volatile(
@@ -444,7 +485,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
               "r"(tc::smem_u32(&bar.k_full[k])), "l"(pol)
               : "memory");
           kq = ++ks;
-          if (!wait_bar(&bar.v_empty[v], ((vs / NV) & 1) ^ 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER)) { ok = false; break; }
+          if (!wait_for(&bar.v_empty[v], ((vs / NV) & 1) ^ 1, &bar.abort_flag, ST_TIMEOUT_PRODUCER)) { ok = false; break; }
           const uint32_t bytes = (uint32_t)min(KT, w.len - t * KT) * 128u;
           tc::mbar_arrive_expect_tx(&bar.v_full[v], bytes);
           asm volatile(
@@ -469,74 +510,71 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       const uint32_t id_o = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((KT >> 4) << 24);  // f16 x f16, B MN-major
       const uint64_t dQ = tc::sdesc_k128(tc::smem_u32(sQ)), dK = tc::sdesc_k128(tc::smem_u32(sK));
       const uint64_t dW = sdesc_mn128(tc::smem_u32(sW), VCHUNK);      // addresses step by bytes >> 4
-      // the S products run up to NB tiles ahead of P V, with a walk of their own
+      // The S products have a walk of their own, up to NB tiles ahead of P V (one S buffer each), but no further than the
+      // unit after the one P V works on: the Q of the unit after that is staged only when the softmax warps have left
+      // this one. S of tile i + NB goes into the buffer of P of tile i, behind its P V in the issue order.
       Walk ws = w;
       int ts = w.ta, te = w.n > 0 ? w.end() : 0;      // next tile of ws, end of its tiles
-      uint32_t k = 0, kph = 0, s6 = 0, seg_s = 0;
-      bool q_ready = false, ok = true;
-      auto issue_s = [&]() -> bool {
-        if (!q_ready) {
-          if (!wait_bar(&bar.q_full, seg_s & 1, abort_flag, a.status, ST_TIMEOUT_MMA)) return false;
-          q_ready = true;
-        }
-        const bool own = ts >= ws.tp && ws.own > 0;
-        const uint32_t d = tS + (s6 >= NB ? s6 - NB : s6) * 128;
-        for (int part = 0; part < (own ? 2 : 1); ++part) {
-          if (!wait_bar(&bar.k_full[k], kph, abort_flag, a.status, ST_TIMEOUT_MMA)) return false;
-          tc::fence_after_sync();
-          const uint64_t dk = dK + k * (KSTAGE >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)      // hi, then lo
-            mma_f8(d, dQ + (kk >> 2) * (KSTAGE >> 4) + (kk & 3) * 2, dk + (kk & 3) * 2, id_s, part != 0 || kk != 0);
-          tc::mma_commit(&bar.k_empty[k]);
-          if (++k == NK) {
-            k = 0;
-            kph ^= 1;
-          }
-        }
-        tc::mma_commit(&bar.s_full[s6]);
-        s6 = s6 == 2 * NB - 1 ? 0 : s6 + 1;
-        if (++ts == te) {
-          tc::mma_commit(&bar.q_empty);
-          ws.next(p);
-          ts = 0;
-          te = ws.n > 0 ? ws.end() : 0;
-          ++seg_s;
-          q_ready = false;
-        }
-        return true;
-      };
-      // up to NB products ahead, but no further than the unit after the one P V works on: the Q of the unit after that
-      // is staged only when the softmax warps have left this one
+      int j = 0, n = te - ts;                         // next tile and number of tiles of w's unit
+      uint32_t k = 0, kph = 0, s6 = 0, seg_s = 0, g = 0, ph = 0, seg = 0;
       int ahead = 0;
-      auto fill = [&](uint32_t seg) {
-        for (; ok && ahead < NB && ws.n > 0 && seg_s <= seg + 1; ++ahead) ok = issue_s();
-      };
-      fill(0);
-      uint32_t g = 0, ph = 0, seg = 0;
-      for (; w.n > 0 && ok; w.next(p), ++seg) {
-        fill(seg);
-        if (seg > 0 && !wait_bar(&bar.o_free, (seg - 1) & 1, abort_flag, a.status, ST_TIMEOUT_MMA)) break;
-        const int n = w.end() - w.ta;
-        for (int j = 0; j < n; ++j) {
-          if (!wait_bar(&bar.w_full[g], ph, abort_flag, a.status, ST_TIMEOUT_MMA) ||
-              !wait_bar(&bar.p_ready[g], ph, abort_flag, a.status, ST_TIMEOUT_MMA)) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
-          const uint64_t dw = dW + g * (VTILE >> 4);
+      bool q_ready = false;
+      while (w.n > 0) {
+        if (ahead < NB && ws.n > 0 && seg_s <= seg + 1) {
+          if (!q_ready && !wait_for(&bar.q_full, seg_s & 1, &bar.abort_flag, ST_TIMEOUT_MMA)) break;
+          q_ready = true;
+          const bool own = ts >= ws.tp && ws.own > 0;
+          const uint32_t d = tS + (s6 >= NB ? s6 - NB : s6) * 128;
+          bool ok = true;
+#pragma unroll 1
+          for (int part = 0; part < (own ? 2 : 1); ++part) {
+            ok = ok && wait_for(&bar.k_full[k], kph, &bar.abort_flag, ST_TIMEOUT_MMA);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint64_t dk = dK + k * (KSTAGE >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc::mma_bf16_tmem_a(tO, tS + g * 128 + kk * 8, dw + kk * (2048 >> 4), id_o, (j != 0 || kk != 0) ? 1u : 0u);
-          tc::mma_commit(&bar.w_empty[g]);
-          --ahead;
-          fill(seg);     // into the buffer of P, behind P V in the issue order
-          if (!ok) break;
-          if (++g == NB) {
-            g = 0;
-            ph ^= 1;
+            for (int kk = 0; kk < 8; ++kk)      // hi, then lo
+              mma_f8(d, dQ + (kk >> 2) * (KSTAGE >> 4) + (kk & 3) * 2, dk + (kk & 3) * 2, id_s, part != 0 || kk != 0);
+            tc::mma_commit(&bar.k_empty[k]);
+            if (++k == NK) {
+              k = 0;
+              kph ^= 1;
+            }
           }
+          if (!ok) break;
+          tc::mma_commit(&bar.s_full[s6]);
+          s6 = s6 == 2 * NB - 1 ? 0 : s6 + 1;
+          ++ahead;
+          if (++ts == te) {
+            tc::mma_commit(&bar.q_empty);
+            ws.next(p);
+            ts = 0;
+            te = ws.n > 0 ? ws.end() : 0;
+            ++seg_s;
+            q_ready = false;
+          }
+          continue;
+        }
+        if (j == 0 && seg > 0 && !wait_for(&bar.o_free, (seg - 1) & 1, &bar.abort_flag, ST_TIMEOUT_MMA)) break;
+        if (!wait_for(&bar.w_full[g], ph, &bar.abort_flag, ST_TIMEOUT_MMA) ||
+            !wait_for(&bar.p_ready[g], ph, &bar.abort_flag, ST_TIMEOUT_MMA))
+          break;
+        tc::fence_after_sync();
+        const uint64_t dw = dW + g * (VTILE >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_bf16_tmem_a(tO, tS + g * 128 + kk * 8, dw + kk * (2048 >> 4), id_o, (j != 0 || kk != 0) ? 1u : 0u);
+        tc::mma_commit(&bar.w_empty[g]);
+        --ahead;
+        if (++g == NB) {
+          g = 0;
+          ph ^= 1;
+        }
+        if (++j == n) {
+          w.next(p);
+          j = 0;
+          n = w.n > 0 ? w.end() : 0;
+          ++seg;
         }
       }
       tc::mma_commit(&bar.done);
@@ -547,14 +585,14 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     // lanes 0-7 K, 8-15 V, one per 16 keys; the next of this warp's tiles is loaded while the last waits for its slot
     Walk w;
     w.start(p, bar.walk);
-    const int64_t runs = (a.cap + a.S - 1) / a.S;
+    const int64_t runs = (a.cap + a.S - 1) >> p.s_shift;
     uint32_t pt = 0;
     float held = 0.f;
     bool have = false;
     uint32_t held_pt = 0;
     auto put = [&]() {
       const uint32_t s = held_pt & 3;
-      wait_bar(&bar.r_empty[s], ((held_pt >> 2) & 1) ^ 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+      wait_for(&bar.r_empty[s], ((held_pt >> 2) & 1) ^ 1, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
       const float v = fmaxf(__shfl_down_sync(0xffffffffu, held, 8), 5.421010862427522e-20f);   // 2^-64
       if (lane < 8) bar.run[s][lane] = make_float4(held, log2f(v), 1.0f / v, 0.f);
       arrive(&bar.r_full[s]);
@@ -566,7 +604,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if ((int)(pt & 1) != warp - 2) continue;
         float x = 0.f;      // 16 keys past the prefix: masked, any finite scale will do
         const int key = t * KT + 16 * (lane & 7);
-        if (lane < 16 && key < w.len) x = (lane < 8 ? a.k_scale : a.v_scale)[bh * runs + key / a.S];
+        if (lane < 16 && key < w.len) x = (lane < 8 ? a.k_scale : a.v_scale)[bh * runs + (key >> p.s_shift)];
         if (have) put();
         held = x;
         held_pt = pt;
@@ -588,7 +626,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       if (seg > 0) {   // the first unit's Q is staged by the softmax warps, which have nothing to do yet
         Quarter q;
         load_q(p, w.b, w.h, w.rt, ct, q);      // before the wait for the previous unit's last S
-        wait_bar(&bar.q_empty, (seg - 1) & 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+        wait_for(&bar.q_empty, (seg - 1) & 1, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
         stage_q(p, w.b, w.h, w.rt, ct, 128, sQ, bar.qscale, q);
         fence_async_smem();
         __syncwarp();
@@ -596,10 +634,10 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       }
       for (int t = w.ta; t < w.end(); ++t) {
         uint8_t* dst = sW + g * VTILE;
-        wait_bar(&bar.w_empty[g], wph, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+        wait_for(&bar.w_empty[g], wph, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
         if (t < w.tp) {
           const int n = min(KT, w.len - t * KT);
-          wait_bar(&bar.v_full[v], vph, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+          wait_for(&bar.v_full[v], vph, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
           const uint8_t* src = sV + v * KSTAGE;
 #pragma unroll 2
           for (int i = 0; i < 8; ++i) {
@@ -654,7 +692,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           const uint32_t k0 = k, k1 = parts == 2 ? (k + 1) % NK : k;
           for (int i = 0; i < parts; ++i) {
             const uint32_t kk = i ? k1 : k0;
-            wait_bar(&bar.k_grant[kk], (granted >> kk) & 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+            wait_for(&bar.k_grant[kk], (granted >> kk) & 1, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
             granted ^= 1u << kk;
           }
           const float ik = kv8::exp2i(-ek), iv = kv8::exp2i(-ev);
@@ -705,9 +743,9 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     for (; w.n > 0; w.next(p), ++seg) {
       const int R = w.rt * KT + row;
       const bool live = R < p.n_rows, warp_live = w.rt * KT + (warp & 3) * 32 < p.n_rows;
-      const int qi = (live ? R : p.n_rows - 1) / p.G;
-      const int own_lim = a.k_own ? (int)min((int64_t)a.Lq, ((int64_t)(qi / a.blk_len) + 1) * a.blk_len) : 0;
-      wait_bar(&bar.q_full, seg & 1, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+      const int qi = p.by_G(live ? R : p.n_rows - 1);
+      const int own_lim = a.k_own ? visible_own(p, qi) : 0;
+      wait_for(&bar.q_full, seg & 1, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
       const float rowc = bar.qscale[row];
       arrive(&bar.q_empty);
       float mg = -INFINITY, l = 0.f;      // the sum of this group's tiles, relative to mg
@@ -719,11 +757,11 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           const int lim = pre ? w.len - t * KT : own_lim - (t - w.tp) * KT;
           // every barrier here is at most one phase behind what is waited for: this group's last tile was it - 2, after
           // the other's it - 3, and S of this tile was issued behind P V of it - 3
-          wait_bar(&bar.s_full[s6], sph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+          wait_for(&bar.s_full[s6], sph, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
           if (pre)
-            wait_bar(&bar.r_full[rs], (pt >> 2) & 1, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+            wait_for(&bar.r_full[rs], (pt >> 2) & 1, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
           else
-            wait_bar(&bar.w_full[g], ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+            wait_for(&bar.w_full[g], ph, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
           if (warp_live) {
             const float4* run = pre ? bar.run[rs] : &bar.run_own[g];
             const int rstep = pre ? 1 : 0;
@@ -757,7 +795,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             const float alpha = prev == now || prev == -INFINITY ? 1.f : ex2(prev - now);
             if (t > w.ta && __any_sync(0xffffffffu, alpha != 1.f)) {
               // O holds the unit's tiles before this one once the last P V completes
-              wait_bar(&bar.w_empty[g == 0 ? NB - 1 : g - 1], g == 0 ? ph ^ 1 : ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+              wait_for(&bar.w_empty[g == 0 ? NB - 1 : g - 1], g == 0 ? ph ^ 1 : ph, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
               __syncwarp();
               tc::fence_after_sync();
 #pragma unroll 1
@@ -804,7 +842,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       bar.ml[seg & 1][grp][row] = make_float2(mg, l);
       tc::named_bar_sync(pair + 8, 64);
       // the unit's last P V (the group of its last tile, now here too, has seen the S behind the one three before it)
-      wait_bar(&bar.w_empty[g == 0 ? NB - 1 : g - 1], g == 0 ? ph ^ 1 : ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+      wait_for(&bar.w_empty[g == 0 ? NB - 1 : g - 1], g == 0 ? ph ^ 1 : ph, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
       if (warp_live) {
         const float2 x0 = bar.ml[seg & 1][0][row], x1 = bar.ml[seg & 1][1][row];
         mg = fmaxf(x0.x, x1.x);           // what O is relative to: the reference never decreases
@@ -858,6 +896,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc(bar.tmem_base, 512);
+    if (lane == 0 && *abort_flag && a.status) atomicExch(a.status, *abort_flag);
   }
 }
 
@@ -993,7 +1032,7 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
         const int bh = w.b * a.Hkv + w.h;
         for (int rt = 0; rt < q_rt && ok; ++rt)
           for (int t = w.ta; t < w.end(); ++t) {
-            if (!wait_bar(&bar.k_empty[k], ph, abort_flag, a.status, ST_TIMEOUT_PRODUCER)) { ok = false; break; }
+            if (!wait_for(&bar.k_empty[k], ph, &bar.abort_flag, ST_TIMEOUT_PRODUCER)) { ok = false; break; }
             tc::mbar_arrive_expect_tx(&bar.k_full[k], KSTAGE);
             asm volatile(
                 "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
@@ -1022,10 +1061,10 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
         for (int rt = 0; rt < q_rt && ok; ++rt, ++seg) {
           const uint32_t qb = seg & 1;
           const uint64_t dq = dQ + qb * (2 * KSTAGE >> 4);
-          if (!wait_bar(&bar.q_full[qb], (seg >> 1) & 1, abort_flag, a.status, ST_TIMEOUT_MMA)) { ok = false; break; }
+          if (!wait_for(&bar.q_full[qb], (seg >> 1) & 1, &bar.abort_flag, ST_TIMEOUT_MMA)) { ok = false; break; }
           for (int n = w.end() - w.ta; n > 0; --n) {
-            if (!wait_bar(&bar.s_empty[sb], sph, abort_flag, a.status, ST_TIMEOUT_MMA) ||
-                !wait_bar(&bar.k_full[k], kph, abort_flag, a.status, ST_TIMEOUT_MMA)) {
+            if (!wait_for(&bar.s_empty[sb], sph, &bar.abort_flag, ST_TIMEOUT_MMA) ||
+                !wait_for(&bar.k_full[k], kph, &bar.abort_flag, ST_TIMEOUT_MMA)) {
               ok = false;
               break;
             }
@@ -1072,13 +1111,13 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
         tc::named_bar_sync(kBarConv, 128);
         const int k = bits_exp(max(max(bar.red[qb][0], bar.red[qb][1]), max(bar.red[qb][2], bar.red[qb][3])));
         const float inv = kv8::exp2i(-k);
-        const int R = rt * KT + ct, qi = R / p.G;
+        const int R = rt * KT + ct, qi = p.by_G(R);
         float nl = -INFINITY;
         if (R < p.n_rows) {
           const float lse = a.lse_in[((int64_t)w.b * a.Lq + qi) * a.Hq + w.h * p.G + R - qi * p.G];
           if (lse != -INFINITY) nl = -lse * kLog2e;
         }
-        if (seg >= 2) wait_bar(&bar.q_empty[qb], ((seg >> 1) & 1) ^ 1, abort_flag, a.status, ST_TIMEOUT_PRODUCER);
+        if (seg >= 2) wait_for(&bar.q_empty[qb], ((seg >> 1) & 1) ^ 1, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
         bar.nlse[qb][ct] = nl;
         if (ct == 0) bar.factor[qb] = kv8::exp2i(k) * (a.scale * kLog2e);
 #pragma unroll 1
@@ -1096,7 +1135,7 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
     // ------------------------------------------------------------------ weights
     const int grp = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const int64_t runs = (a.cap + a.S - 1) / a.S;
+    const int64_t runs = (a.cap + a.S - 1) >> p.s_shift;
     uint32_t it = 0, sb = 0, ph = 0, seg = 0;
     for (; w.n > 0; w.next(p)) {
       const int64_t bh = (int64_t)w.b * a.Hkv + w.h;
@@ -1104,7 +1143,7 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
       for (int rt = 0; rt < q_rt; ++rt, ++seg) {
         const uint32_t qb = seg & 1;
         const int cols = min(KT, p.n_rows - rt * KT);
-        wait_bar(&bar.q_full[qb], (seg >> 1) & 1, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+        wait_for(&bar.q_full[qb], (seg >> 1) & 1, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
         const float f = bar.factor[qb];
         // the other group may have added the last row tile to this group's tiles
         if (rt > 0) tc::named_bar_sync(kBarPair, 256);
@@ -1115,11 +1154,11 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
             float ks = 0.f, old = 0.f;
             const int64_t at = bh * a.cap + key;
             if (live) {
-              ks = a.k_scale[bh * runs + key / a.S];
+              ks = a.k_scale[bh * runs + (key >> p.s_shift)];
               if (rt > 0) old = a.mass_out[at];
               else if (a.mass_in) old = a.decay * a.mass_in[at];
             }
-            wait_bar(&bar.s_full[sb], ph, abort_flag, a.status, ST_TIMEOUT_EPILOGUE);
+            wait_for(&bar.s_full[sb], ph, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
             __syncwarp();
             tc::fence_after_sync();
             const float c = f * ks;
@@ -1159,6 +1198,7 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc(bar.tmem_base, 512);
+    if (lane == 0 && *abort_flag && a.status) atomicExch(a.status, *abort_flag);
   }
 }
 
@@ -1179,6 +1219,15 @@ int encode_codes(CUtensorMap* m, const void* codes, int64_t cap, int64_t bh) {
     return DLLM_ERR_CUDA;
   }
   return DLLM_OK;
+}
+
+void set_shape(Params& p) {
+  p.G = p.a.Hq / p.a.Hkv;
+  p.n_rows = p.a.Lq * p.G;
+  p.a.blk_len = std::min(p.a.blk_len, p.a.Lq);     // a longer block is the whole of the queries all the same
+  p.by_G = fast_div(p.G);
+  p.by_blk = fast_div(p.a.blk_len);
+  p.s_shift = p.a.S == 16 ? 4 : p.a.S == 32 ? 5 : p.a.S == 64 ? 6 : 7;
 }
 
 // Own key tiles of all row tiles (own_keys on the host).
@@ -1203,8 +1252,7 @@ size_t attn_kv8_tc_workspace_bytes(int B, int Lq, int Hq, int Hkv) {
 int launch_attn_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
   Params p;
   p.a = a;
-  p.G = a.Hq / a.Hkv;
-  p.n_rows = a.Lq * p.G;
+  set_shape(p);
   p.n_rt = (p.n_rows + KT - 1) / KT;
   p.own_sum = own_tiles_sum(a, p.n_rt, p.G);
   p.part = static_cast<float*>(a.ws);
@@ -1234,8 +1282,7 @@ int launch_attn_mass_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
   Params p = {};
   p.a = a;
   p.a.k_own = nullptr;
-  p.G = a.Hq / a.Hkv;
-  p.n_rows = a.Lq * p.G;
+  set_shape(p);
   p.n_rt = 1;                  // units of the walk are whole (b, kv head)s
   const int64_t most = (int64_t)a.B * a.Hkv * ((a.P + KT - 1) / KT);
   p.n_cta = (int)std::min<int64_t>(num_sms(), most);
