@@ -16,20 +16,20 @@
 //               four products).
 //   softmax     one thread per row; x = S * (2^k scale log2(e) k_scale) + log2(v_scale) - m: the V scale of each run rides
 //               in the exponent, so that P V needs no scaled copy of V; the row sum divides it out again run by run.
-//               P = 2^(x + 2) as f16, with m within 2^13 of the largest score so far: the largest weight is in [2^2, 2^15],
-//               a weight keeps 11 bits down to 2^-16 of it and is dropped below 2^-27 (n keys lose at most n 2^-27 of the
-//               largest weight). A move of m waits for the tensor pipe and costs about 5000 clocks; at 2^8 a third of the
-//               tiles of normal scores moved it for some row.
+//               P = 2^(x + 2) as f16. The reference m is not a running maximum: it is the largest of the first 32 scores
+//               that a row sees, and moves (rescaling O and the P of the tile so far) only when 32 weights add up to more
+//               than 30000, that is before one could leave f16's range. So the scores are read once, and no maximum is
+//               taken on the way. A weight keeps 11 bits down to 2^-16 of the reference and is dropped below 2^-27 (n
+//               keys lose at most n 2^-27 of the largest weight).
 //   O += P V    kind::f16 with A = P from TMEM and B = V as f16 (every E4M3 value is one), written from the codes by four
 //               converter warps into the MN-major layout.
 // Tensor time of a tile: 8 + 8 MMAs of 64 clocks, and about 250 clocks for each of the two changes of the instruction
 // descriptor (measured on bare loops: 512 clocks per 8 MMAs of one kind, 756 when S and P V alternate, whatever their
 // operand sources), so about 1510 clocks, against 1420 for the tile's bytes at one SM's share of the HBM rate and 1024
-// for its exponentials. Three S buffers and one O in TMEM keep three tiles in flight, so that the tensor pipe does not
-// wait for a softmax. Two softmax groups of four warps take alternate tiles, one thread per row, so that the exponentials
-// of one overlap the loads, maxima and barriers of the other (two threads per row on the same tile took 2700 clocks a
-// tile, 1500 of them exponentials). The row's reference maximum is common to both: a group passes it on to the other's
-// next tile as soon as it knows its own tile's maximum, and moves it (rescaling O) only when that exceeds it by 2^13.
+// for its exponentials. Two softmax groups of four warps take alternate tiles, one thread per row, each with an S and an O
+// of its own in TMEM and references of its own; their results are joined at the end of a unit. Measured on the way, 8
+// rows of 32768 keys, 512 query rows a kv head: two threads per row on the same tile 134 us; one O with a reference that
+// the groups pass on to each other and a pass for the maximum 105 us.
 //
 // Roles: warp 0 TMA, warp 1 MMA, warps 2 and 3 the runs' scales (alternate prefix tiles), warps 4-7 and 8-11 softmax (even
 // and odd tiles), warps 12-15 convert Q, V and the own rows. Warps whose rows are all past the last only
@@ -49,12 +49,11 @@ constexpr int KT = 128;                    // keys per tile = rows per unit
 constexpr int KSTAGE = 128 * 128;          // K or V codes of a tile: 16 KB
 constexpr int VTILE = 2 * 128 * 64 * 2;    // V of a tile as f16: two 64-wide chunks of 16 KB
 constexpr int VCHUNK = VTILE / 2;
-constexpr int NK = 3, NV = 2, NB = 3;      // stages of the K and V code rings; S and f16 V buffers
-constexpr float kRescale = 13.f;           // the reference maximum moves when a tile exceeds it by 2^13
-constexpr float kOff = 2.f;                // P is 2^2 times the weight relative to the reference maximum
+constexpr int NK = 3, NV = 2, NB = 3;      // stages of the K and V code rings; f16 V buffers
+constexpr float kMost = 30000.f;           // 32 weights that add up to more move the reference
+constexpr float kOff = 2.f;                // P is 2^2 times the weight relative to the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// named barriers: the 128 converter threads; then three for the two warps of rows 32 i ..: a reference maximum from group 0
-// to group 1, from group 1 to group 0, and both at the end of a unit
+// named barriers: the 128 converter threads; 2 + i: the two warps of rows 32 i ..
 constexpr int kBarConv = 1, kBarPair = 2;
 constexpr int kPart = 33 * 128 * 4;        // floats of one partial result: 32 float4 columns and (m, l, -, -), by row
 
@@ -102,7 +101,7 @@ struct Bars {
   uint64_t k_grant[NK];                    // a free K stage handed to the converters, for own rows
   uint64_t v_full[NV], v_empty[NV];
   uint64_t w_full[NB], w_empty[NB];        // f16 V of a tile; empty = the tile's P V is complete
-  uint64_t s_full[2 * NB], p_ready[NB];    // S of tile i: barrier i mod 6, so that one group alone waits for each
+  uint64_t s_full[2], p_ready[2];          // per softmax group
   uint64_t r_full[4], r_empty[4];          // scales of a prefix tile
   uint64_t o_free;                         // O of the finished unit has been read
   uint64_t done;
@@ -113,8 +112,7 @@ struct Bars {
   float qscale[KT];                        // per row: 2^k * scale * log2(e)
   float4 run[4][8];                        // per prefix tile and 16 keys: k scale, log2(v scale), 1 / v scale
   float4 run_own[NB];                      // of an own tile
-  float ref[2][KT];                        // [tile parity][row]: reference maximum passed on
-  float2 ml[2][2][KT];                     // [unit parity][group][row]: reference maximum and sum
+  float2 ml[2][2][KT];                     // [unit parity][group][row]: reference and sum
 };
 constexpr int SMEM = 1024 + 2 * KSTAGE /*Q*/ + NK * KSTAGE + NV * KSTAGE + NB * VTILE + (int)sizeof(Bars);
 static_assert(SMEM <= 232448, "shared memory budget");
@@ -358,10 +356,10 @@ DLLM_DEV float scores_max(const float* v, float rowc, const float4* run, int rst
   }
   return mt;
 }
-// P of 32 columns as f16 pairs, to 16 columns of TMEM; returns the sum of the weights with the V scales divided out.
-DLLM_DEV float scores_exp(const float* v, float rowc, const float4* run, int rstep, float shift, uint32_t at) {
-  float l = 0.f;
-  uint32_t pk[16];
+// The weights of 32 columns as f16 pairs, their sum, and their sum with the V scales divided out (l).
+DLLM_DEV float scores_exp(const float* v, float rowc, const float4* run, int rstep, float shift, uint32_t* pk, float& l) {
+  float all = 0.f;
+  l = 0.f;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const float4 rs = run[u * rstep];
@@ -378,16 +376,38 @@ DLLM_DEV float scores_exp(const float* v, float rowc, const float4* run, int rst
     }
     float s0, s1;
     upk2(s2, s0, s1);
+    all += s0 + s1;
     l = fmaf(s0 + s1, rs.z, l);
   }
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
-      "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7]), "r"(pk[8]),
-      "r"(pk[9]), "r"(pk[10]), "r"(pk[11]), "r"(pk[12]), "r"(pk[13]), "r"(pk[14]), "r"(pk[15])
-      : "memory");
-  return l;
+  return all;
 }
-DLLM_DEV void named_bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+// n groups of 8 TMEM columns of a row times alpha, as fp32 or as pairs of f16.
+template <bool F16>
+DLLM_DEV void scale_columns(uint32_t at, int n, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < n; ++c, at += 8) {
+    uint32_t x[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+                 : "r"(at)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (F16) {
+        // in fp32: alpha is mostly below f16's normal range
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
+        x[i] = f16x2(y.x * alpha, y.y * alpha);
+      } else {
+        x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
+      }
+    }
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(x[0]), "r"(x[1]),
+                 "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  }
+  tc::tmem_st_wait();
+}
 DLLM_DEV void arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar)), "r"(n) : "memory");
 }
@@ -420,8 +440,9 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     for (int i = 0; i < NB; ++i) {
       tc::mbar_init(&bar.w_full[i], 4);
       tc::mbar_init(&bar.w_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bar.s_full[i], 1);
-      tc::mbar_init(&bar.s_full[NB + i], 1);
       tc::mbar_init(&bar.p_ready[i], 4);
     }
     for (int i = 0; i < 4; ++i) {
@@ -442,7 +463,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   __syncthreads();
   pdl_wait();
   volatile int* abort_flag = &bar.abort_flag;
-  const uint32_t tS = bar.tmem_base, tO = bar.tmem_base + NB * 128;
+  const uint32_t tS = bar.tmem_base, tO = bar.tmem_base + 256;      // S_0, S_1; O_0, O_1
   auto arrive = [&](uint64_t* b) {       // once for the warp, after all its lanes
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(b);
@@ -510,21 +531,21 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       const uint32_t id_o = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((KT >> 4) << 24);  // f16 x f16, B MN-major
       const uint64_t dQ = tc::sdesc_k128(tc::smem_u32(sQ)), dK = tc::sdesc_k128(tc::smem_u32(sK));
       const uint64_t dW = sdesc_mn128(tc::smem_u32(sW), VCHUNK);      // addresses step by bytes >> 4
-      // The S products have a walk of their own, up to NB tiles ahead of P V (one S buffer each), but no further than the
-      // unit after the one P V works on: the Q of the unit after that is staged only when the softmax warps have left
-      // this one. S of tile i + NB goes into the buffer of P of tile i, behind its P V in the issue order.
+      // The S products have a walk of their own, up to two tiles ahead of P V, but no further than the unit after the one
+      // P V works on: the Q of the unit after that is staged only when the softmax warps have left this one. S of tile
+      // i + 2 goes into the buffer of P of tile i, behind its P V in the issue order.
       Walk ws = w;
       int ts = w.ta, te = w.n > 0 ? w.end() : 0;      // next tile of ws, end of its tiles
       int j = 0, n = te - ts;                         // next tile and number of tiles of w's unit
-      uint32_t k = 0, kph = 0, s6 = 0, seg_s = 0, g = 0, ph = 0, seg = 0;
+      uint32_t k = 0, kph = 0, it_s = 0, seg_s = 0, it = 0, g = 0, ph = 0, seg = 0;
       int ahead = 0;
       bool q_ready = false;
       while (w.n > 0) {
-        if (ahead < NB && ws.n > 0 && seg_s <= seg + 1) {
+        if (ahead < 2 && ws.n > 0 && seg_s <= seg + 1) {
           if (!q_ready && !wait_for(&bar.q_full, seg_s & 1, &bar.abort_flag, ST_TIMEOUT_MMA)) break;
           q_ready = true;
           const bool own = ts >= ws.tp && ws.own > 0;
-          const uint32_t d = tS + (s6 >= NB ? s6 - NB : s6) * 128;
+          const uint32_t d = tS + (it_s & 1) * 128;
           bool ok = true;
 #pragma unroll 1
           for (int part = 0; part < (own ? 2 : 1); ++part) {
@@ -542,8 +563,8 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             }
           }
           if (!ok) break;
-          tc::mma_commit(&bar.s_full[s6]);
-          s6 = s6 == 2 * NB - 1 ? 0 : s6 + 1;
+          tc::mma_commit(&bar.s_full[it_s & 1]);
+          ++it_s;
           ++ahead;
           if (++ts == te) {
             tc::mma_commit(&bar.q_empty);
@@ -557,15 +578,17 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         if (j == 0 && seg > 0 && !wait_for(&bar.o_free, (seg - 1) & 1, &bar.abort_flag, ST_TIMEOUT_MMA)) break;
         if (!wait_for(&bar.w_full[g], ph, &bar.abort_flag, ST_TIMEOUT_MMA) ||
-            !wait_for(&bar.p_ready[g], ph, &bar.abort_flag, ST_TIMEOUT_MMA))
+            !wait_for(&bar.p_ready[it & 1], (it >> 1) & 1, &bar.abort_flag, ST_TIMEOUT_MMA))
           break;
         tc::fence_after_sync();
         const uint64_t dw = dW + g * (VTILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          tc::mma_bf16_tmem_a(tO, tS + g * 128 + kk * 8, dw + kk * (2048 >> 4), id_o, (j != 0 || kk != 0) ? 1u : 0u);
+          tc::mma_bf16_tmem_a(tO + (it & 1) * 128, tS + (it & 1) * 128 + kk * 8, dw + kk * (2048 >> 4), id_o,
+                              (j >= 2 || kk != 0) ? 1u : 0u);
         tc::mma_commit(&bar.w_empty[g]);
         --ahead;
+        ++it;
         if (++g == NB) {
           g = 0;
           ph ^= 1;
@@ -732,7 +755,8 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     w.start(p, bar.walk);
     const int grp = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, pair = kBarPair + (warp & 3);
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    uint32_t it = 0, g = 0, ph = 0, s6 = 0, sph = 0, pt = 0, seg = 0;
+    const uint32_t tSg = tS + grp * 128 + lane_off, tOg = tO + grp * 128 + lane_off;
+    uint32_t it = 0, g = 0, ph = 0, pt = 0, seg = 0;
     if (w.n > 0) {
       Quarter q;
       load_q(p, w.b, w.h, w.rt, tid - 128, q);
@@ -748,16 +772,18 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       wait_for(&bar.q_full, seg & 1, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
       const float rowc = bar.qscale[row];
       arrive(&bar.q_empty);
-      float mg = -INFINITY, l = 0.f;      // the sum of this group's tiles, relative to mg
+      float mg = -INFINITY, l = 0.f;      // reference and sum of this group's tiles
+      uint32_t lastg = 0, lastph = 0;     // V buffer and phase of the group's last tile
+      bool any = false;                   // the group has had a tile of this unit
       const int t_end = w.end();
       for (int t = w.ta; t < t_end; ++t, ++it) {
         const bool pre = t < w.tp;
         if ((int)(it & 1) == grp) {
           const uint32_t rs = pt & 3;
           const int lim = pre ? w.len - t * KT : own_lim - (t - w.tp) * KT;
-          // every barrier here is at most one phase behind what is waited for: this group's last tile was it - 2, after
-          // the other's it - 3, and S of this tile was issued behind P V of it - 3
-          wait_for(&bar.s_full[s6], sph, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
+          // S of this tile was issued behind P V of the tiles it - 2 (whose O is therefore complete) and it - 3, so no
+          // barrier waited for here is more than one phase behind
+          wait_for(&bar.s_full[grp], (it >> 1) & 1, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
           if (pre)
             wait_for(&bar.r_full[rs], (pt >> 2) & 1, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
           else
@@ -765,88 +791,71 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           if (warp_live) {
             const float4* run = pre ? bar.run[rs] : &bar.run_own[g];
             const int rstep = pre ? 1 : 0;
-            tc::fence_after_sync();
-            const uint32_t tSg = tS + g * 128 + lane_off;
             const bool partly = !__all_sync(0xffffffffu, lim >= KT);
-            // the row of S is read twice, 32 columns at a time, for its maximum and for its weights: loops this short stay
-            // in the instruction caches, which four kinds of warps share (the same code unrolled over 128 columns took
-            // 10 % longer). P takes half the columns of the scores that it replaces, all read by then.
-            float mt = -INFINITY;
+            tc::fence_after_sync();
+            // 32 columns at a time, P into half the columns of the scores that it replaces
+            float lt = 0.f;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               float v[32];
               load_scores(tSg + 32 * c, partly, lim - 32 * c, v);
-              mt = fmaxf(mt, scores_max(v, rowc, run + 2 * c * rstep, rstep));
-            }
-            float prev = -INFINITY;
-            if (t > w.ta) {
-              tc::named_bar_sync(pair + 4 * (grp ^ 1), 64);
-              prev = bar.ref[(it & 1) ^ 1][row];
-            }
-            const float now = mt > prev + kRescale ? mt : prev;
-            if (t + 1 < t_end) {
-              bar.ref[it & 1][row] = now;
-              named_bar_arrive(pair + 4 * grp, 64);
-            }
-            if (mg != now) {
-              l *= ex2(mg - now);
-              mg = now;
-            }
-            const float alpha = prev == now || prev == -INFINITY ? 1.f : ex2(prev - now);
-            if (t > w.ta && __any_sync(0xffffffffu, alpha != 1.f)) {
-              // O holds the unit's tiles before this one once the last P V completes
-              wait_for(&bar.w_empty[g == 0 ? NB - 1 : g - 1], g == 0 ? ph ^ 1 : ph, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
-              __syncwarp();
-              tc::fence_after_sync();
+              uint32_t pk[16];
+              float lc;
 #pragma unroll 1
-              for (int c = 0; c < 16; ++c) {      // 8 columns at a time: the scores stay in registers meanwhile
-                const uint32_t at = tO + 8 * c + lane_off;
-                uint32_t x[8];
-                asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-                             "tcgen05.wait::ld.sync.aligned;"
-                             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
-                               "=r"(x[7])
-                             : "r"(at)
-                             : "memory");
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
-                asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
-                             "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-                             : "memory");
+              for (int tries = 0;; ++tries) {
+                const float sum = scores_exp(v, rowc, run + 2 * c * rstep, rstep, kOff - (mg == -INFINITY ? 0.f : mg), pk, lc);
+                const bool move = sum > kMost || mg == -INFINITY;
+                if (tries || !__any_sync(0xffffffffu, move)) break;
+                // the reference of the rows concerned moves to the largest score here, and what they have so far with it
+                const float m = scores_max(v, rowc, run + 2 * c * rstep, rstep);
+                float alpha = 1.f;
+                if (move && m > mg) {
+                  alpha = mg == -INFINITY ? 1.f : ex2(mg - m);
+                  mg = m;
+                }
+                l *= alpha;
+                lt *= alpha;
+                if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                  tc::tmem_st_wait();
+                  scale_columns<true>(tSg, 2 * c, alpha);
+                  if (any) scale_columns<false>(tOg, 16, alpha);
+                }
               }
+              lt += lc;
+              asm volatile(
+                  "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::
+                      "r"(tSg + 16 * c),
+                  "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7]), "r"(pk[8]),
+                  "r"(pk[9]), "r"(pk[10]), "r"(pk[11]), "r"(pk[12]), "r"(pk[13]), "r"(pk[14]), "r"(pk[15])
+                  : "memory");
             }
-            const float shift = kOff - (mg == -INFINITY ? 0.f : mg);
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              float v[32];
-              load_scores(tSg + 32 * c, partly, lim - 32 * c, v);
-              l += scores_exp(v, rowc, run + 2 * c * rstep, rstep, shift, tSg + 16 * c);
-            }
+            l += lt;
             tc::tmem_st_wait();
             tc::fence_before_sync();
           }
-          arrive(&bar.p_ready[g]);
+          arrive(&bar.p_ready[grp]);
           if (pre && lane == 0) tc::mbar_arrive(&bar.r_empty[rs]);
+          any = true;
+          lastg = g;
+          lastph = ph;
         }
         pt += pre;
         if (++g == NB) {
           g = 0;
           ph ^= 1;
         }
-        if (++s6 == 2 * NB) {
-          s6 = 0;
-          sph ^= 1;
-        }
       }
-      const bool whole = w.ta == 0 && w.end() == w.tiles;
+      // this group's last P V, then the other's too
+      if (any) wait_for(&bar.w_empty[lastg], lastph, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
       bar.ml[seg & 1][grp][row] = make_float2(mg, l);
-      tc::named_bar_sync(pair + 8, 64);
-      // the unit's last P V (the group of its last tile, now here too, has seen the S behind the one three before it)
-      wait_for(&bar.w_empty[g == 0 ? NB - 1 : g - 1], g == 0 ? ph ^ 1 : ph, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
+      tc::fence_before_sync();
+      tc::named_bar_sync(pair, 64);
+      const bool whole = w.ta == 0 && w.end() == w.tiles;
       if (warp_live) {
         const float2 x0 = bar.ml[seg & 1][0][row], x1 = bar.ml[seg & 1][1][row];
-        mg = fmaxf(x0.x, x1.x);           // what O is relative to: the reference never decreases
-        const float L = (x0.x == mg ? x0.y : x0.y * ex2(x0.x - mg)) + (x1.x == mg ? x1.y : x1.y * ex2(x1.x - mg));
+        mg = fmaxf(x0.x, x1.x);
+        const float wa = x0.x == -INFINITY ? 0.f : ex2(x0.x - mg), wb = x1.x == -INFINITY ? 0.f : ex2(x1.x - mg);
+        const float L = fmaf(wa, x0.y, wb * x1.y);
         const float inv = L == 0.f ? 0.f : 1.0f / L;
         const bool put = !*abort_flag && live;
         const int64_t qh = ((int64_t)w.b * a.Lq + qi) * a.Hq + w.h * p.G + (live ? R - qi * p.G : 0);
@@ -856,8 +865,12 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int col = 64 * grp + 32 * c;
-          float o[32];
+          float o[32], x[32];
+          // a group without a tile here has left nothing (or another unit's rows) in its O: weight 0 does not read it
           tmem_ld32(tO + col + lane_off, o);
+          tmem_ld32(tO + 128 + col + lane_off, x);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = (wa != 0.f ? wa * o[i] : 0.f) + (wb != 0.f ? wb * x[i] : 0.f);
           if (put && whole) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + qh * 128 + col);
 #pragma unroll
