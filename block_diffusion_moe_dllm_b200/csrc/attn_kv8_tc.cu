@@ -49,7 +49,7 @@ constexpr int KT = 128;                    // keys per tile = rows per unit
 constexpr int KSTAGE = 128 * 128;          // K or V codes of a tile: 16 KB
 constexpr int VTILE = 2 * 128 * 64 * 2;    // V of a tile as f16: two 64-wide chunks of 16 KB
 constexpr int VCHUNK = VTILE / 2;
-constexpr int NK = 3, NV = 2, NB = 3;      // stages of the K and V code rings; f16 V buffers
+constexpr int NK = 3, NV = 4, NB = 2;      // stages of the K and V code rings; f16 V buffers
 constexpr float kMost = 30000.f;           // 32 weights that add up to more move the reference
 constexpr float kOff = 2.f;                // P is 2^2 times the weight relative to the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -413,7 +413,8 @@ DLLM_DEV void arrive_n(uint64_t* bar, uint32_t n) {
 }
 
 __global__ void __launch_bounds__(NT, 1)
-attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ Params p) {
+attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = base;                          // hi, lo
@@ -453,6 +454,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     tc::mbar_init(&bar.done, 1);
     tc::fence_mbar_init();
     tc::prefetch_tmap(&tm_k);
+    tc::prefetch_tmap(&tm_v);
   }
   if (warp == 1) tc::tmem_alloc(&bar.tmem_base, 512);
   pdl_trigger();
@@ -483,8 +485,17 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       uint32_t ks = 0, vs = 0;      // slots of the K and V rings so far
       uint32_t kq = 0, vq = 0;      // one past the last slot that this thread filled (for the drain)
       bool ok = true;
+      // 128 rows of codes: rows past the cache read as zeros, rows past the prefix are masked (K) or cleared (V)
+      auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full, int row, int bh) {
+        tc::mbar_arrive_expect_tx(full, KSTAGE);
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(tc::smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(bh), "r"(tc::smem_u32(full)), "l"(pol)
+            : "memory");
+      };
       for (; w.n > 0 && ok; w.next(p)) {
-        const int64_t bh = (int64_t)w.b * a.Hkv + w.h;
+        const int bh = w.b * a.Hkv + w.h;
         for (int t = w.ta; t < w.end() && ok; ++t) {
           if (t >= w.tp) {
             // own rows: the converters write two K stages (V goes past the code ring). This thread alone waits for
@@ -497,23 +508,10 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           }
           const uint32_t k = ks % NK, v = vs % NV;
           if (!wait_for(&bar.k_empty[k], ((ks / NK) & 1) ^ 1, &bar.abort_flag, ST_TIMEOUT_PRODUCER)) { ok = false; break; }
-          tc::mbar_arrive_expect_tx(&bar.k_full[k], KSTAGE);
-          // rows past the cache read as zeros, rows past the prefix are masked
-          asm volatile(
-              "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-              " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(tc::smem_u32(sK + k * KSTAGE)),
-              "l"(reinterpret_cast<uint64_t>(&tm_k)), "r"(0), "r"(t * KT), "r"((int)bh),
-              "r"(tc::smem_u32(&bar.k_full[k])), "l"(pol)
-              : "memory");
+          load(&tm_k, sK + k * KSTAGE, &bar.k_full[k], t * KT, bh);
           kq = ++ks;
           if (!wait_for(&bar.v_empty[v], ((vs / NV) & 1) ^ 1, &bar.abort_flag, ST_TIMEOUT_PRODUCER)) { ok = false; break; }
-          const uint32_t bytes = (uint32_t)min(KT, w.len - t * KT) * 128u;
-          tc::mbar_arrive_expect_tx(&bar.v_full[v], bytes);
-          asm volatile(
-              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::
-                  "r"(tc::smem_u32(sV + v * KSTAGE)),
-              "l"(a.v_codes + (bh * a.cap + (int64_t)t * KT) * 128), "r"(bytes), "r"(tc::smem_u32(&bar.v_full[v])), "l"(pol)
-              : "memory");
+          load(&tm_v, sV + v * KSTAGE, &bar.v_full[v], t * KT, bh);
           vq = ++vs;
         }
       }
@@ -661,24 +659,26 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if (t < w.tp) {
           const int n = min(KT, w.len - t * KT);
           wait_for(&bar.v_full[v], vph, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
-          const uint8_t* src = sV + v * KSTAGE;
+          // Eight neighbouring lanes take the same 16 columns of eight neighbouring keys: with the 128-byte swizzle on both
+          // sides their 16-byte pieces fall on different banks, and every address is a lane's own plus a constant.
+          const int x = lane & 7, e = lane >> 3, key0 = x + 8 * (int)cw;
+          const uint8_t* src = sV + v * KSTAGE + key0 * 128 + ((e ^ x) << 4);
+          uint8_t* out = dst + key0 * 128;
+          const int o0 = ((2 * e) ^ x) << 4, o1 = ((2 * e + 1) ^ x) << 4;
 #pragma unroll 2
-          for (int i = 0; i < 8; ++i) {
-            const int id = i * 128 + ct, key = id >> 3, e = id & 7;      // 16 codes: key, columns 16 e ..
-            uint4 u = *reinterpret_cast<const uint4*>(src + id * 16);
-            if (key >= n) u = make_uint4(0, 0, 0, 0);    // not loaded: weight 0 times anything but NaN
-            uint32_t h[8];
-            kv8::e4m3x4_to_f16x4(u.x, h[0], h[1]);
-            kv8::e4m3x4_to_f16x4(u.y, h[2], h[3]);
-            kv8::e4m3x4_to_f16x4(u.z, h[4], h[5]);
-            kv8::e4m3x4_to_f16x4(u.w, h[6], h[7]);
-            // granules 2 (e & 3) and the next of chunk e >> 2; the upper half-group writes them in the other order, so
-            // that the eight lanes of a key touch eight different 16-byte columns
-            uint8_t* row = dst + (e >> 2) * VCHUNK + key * 128;
-            const int g0 = (e & 3) * 2, sw = e >> 2;
-            const uint4 x0 = make_uint4(h[0], h[1], h[2], h[3]), x1 = make_uint4(h[4], h[5], h[6], h[7]);
-            *reinterpret_cast<uint4*>(row + (((g0 + sw) ^ (key & 7)) << 4)) = sw ? x1 : x0;
-            *reinterpret_cast<uint4*>(row + (((g0 + 1 - sw) ^ (key & 7)) << 4)) = sw ? x0 : x1;
+          for (int i = 0; i < 4; ++i) {          // keys key0 + 32 i
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {        // columns 16 (e + 4 c) .. of the key: half of chunk c
+              uint4 u = *reinterpret_cast<const uint4*>(src + i * 4096 + (c ? ((e ^ x) & 4 ? -64 : 64) : 0));
+              if (n < KT && key0 + 32 * i >= n) u = make_uint4(0, 0, 0, 0);    // past the prefix: 0 times anything but NaN
+              uint32_t h[8];
+              kv8::e4m3x4_to_f16x4(u.x, h[0], h[1]);
+              kv8::e4m3x4_to_f16x4(u.y, h[2], h[3]);
+              kv8::e4m3x4_to_f16x4(u.z, h[4], h[5]);
+              kv8::e4m3x4_to_f16x4(u.w, h[6], h[7]);
+              *reinterpret_cast<uint4*>(out + c * VCHUNK + i * 4096 + o0) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(out + c * VCHUNK + i * 4096 + o1) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
           }
           arrive(&bar.v_empty[v]);
           if (++v == NV) {
@@ -781,7 +781,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if ((int)(it & 1) == grp) {
           const uint32_t rs = pt & 3;
           const int lim = pre ? w.len - t * KT : own_lim - (t - w.tp) * KT;
-          // S of this tile was issued behind P V of the tiles it - 2 (whose O is therefore complete) and it - 3, so no
+          // S of this tile was issued behind P V of tile it - 2, the last one of this group, so its O is complete and no
           // barrier waited for here is more than one phase behind
           wait_for(&bar.s_full[grp], (it >> 1) & 1, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
           if (pre)
@@ -1276,13 +1276,15 @@ int launch_attn_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
   const int64_t most = (int64_t)a.B * a.Hkv * (p.n_rt * (a.k_own ? tp : std::max<int64_t>(tp, 1)) + p.own_sum);
   DLLM_REQUIRE(most < (1ll << 31), DLLM_ERR_UNSUPPORTED, "block_attn_kv8: too many rows and keys for one call");
   p.n_cta = (int)std::min<int64_t>(num_sms(), most);
-  CUtensorMap mk;
-  // without prefix rows no tile is loaded; the map then describes the queries' memory, which exists
+  CUtensorMap mk, mv;
+  // without prefix rows no tile is loaded; the maps then describe the queries' memory, which exists
   int st = a.P > 0 ? encode_codes(&mk, a.k_codes, a.cap, (int64_t)a.B * a.Hkv) : encode_codes(&mk, a.q, 1, 1);
+  if (st) return st;
+  st = a.P > 0 ? encode_codes(&mv, a.v_codes, a.cap, (int64_t)a.B * a.Hkv) : encode_codes(&mv, a.q, 1, 1);
   if (st) return st;
   st = set_max_smem<attn_kv8_tc_kernel>(SMEM);
   if (st) return st;
-  launch_pdl(attn_kv8_tc_kernel, p.n_cta, NT, SMEM, s, mk, p);
+  launch_pdl(attn_kv8_tc_kernel, p.n_cta, NT, SMEM, s, mk, mv, p);
   DLLM_CHECK_LAUNCH("attn_kv8_tc_kernel");
   if (p.n_cta > 1) {
     launch_pdl(attn_kv8_merge_kernel, (unsigned)((int64_t)a.B * a.Hkv * p.n_rt * (128 / kMergeCols)), KT, 0, s, p);
