@@ -913,9 +913,9 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   }
 }
 
-// Joins the partial results of the units that span several CTAs: one block per unit and 16 output columns, one thread
-// per row, the CTAs in order.
-constexpr int kMergeCols = 16;
+// Joins the partial results of the units that span several CTAs: one block per unit and 8 output columns, one thread
+// per row, the CTAs in order. Bound by the latency of its loads.
+constexpr int kMergeCols = 8;
 __global__ void __launch_bounds__(KT) attn_kv8_merge_kernel(const __grid_constant__ Params p) {
   pdl_enter();
   const Kv8AttnArgs& a = p.a;
@@ -927,30 +927,48 @@ __global__ void __launch_bounds__(KT) attn_kv8_merge_kernel(const __grid_constan
   auto slot = [&](int k) {
     return reinterpret_cast<const float4*>(p.part) + ((int64_t)(sp.x + k) * 2 + (k == 0 ? 1 : 0)) * (kPart / 4);
   };
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) M = fmaxf(M, slot(k)[32 * KT + row].x);
-  float L = 0.f, o[kMergeCols];
+  // one pass, kBatch partial results in flight, against the largest reference so far
+  constexpr int kBatch = 8;
+  float M = -INFINITY, L = 0.f, o[kMergeCols];
 #pragma unroll
   for (int i = 0; i < kMergeCols; ++i) o[i] = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float4* s = slot(k);
-    const float4 ml = s[32 * KT + row];
-    const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-    L = fmaf(wt, ml.y, L);
+#pragma unroll 1
+  for (int k0 = 0; k0 < n; k0 += kBatch) {
+    float2 ml[kBatch];
+    float4 x[kBatch][kMergeCols / 4];
 #pragma unroll
-    for (int i = 0; i < kMergeCols / 4; ++i) {
-      const float4 x = s[(part_col * (kMergeCols / 4) + i) * KT + row];
-      o[4 * i] = fmaf(wt, x.x, o[4 * i]);
-      o[4 * i + 1] = fmaf(wt, x.y, o[4 * i + 1]);
-      o[4 * i + 2] = fmaf(wt, x.z, o[4 * i + 2]);
-      o[4 * i + 3] = fmaf(wt, x.w, o[4 * i + 3]);
+    for (int k = 0; k < kBatch; ++k) {
+      const bool in = k0 + k < n;
+      const float4* s = slot(in ? k0 + k : k0);
+      ml[k] = *reinterpret_cast<const float2*>(s + 32 * KT + row);
+      if (!in) ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i < kMergeCols / 4; ++i) x[k][i] = s[(part_col * (kMergeCols / 4) + i) * KT + row];
+    }
+    float now = M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) now = fmaxf(now, ml[k].x);
+    const float old = M == -INFINITY ? 0.f : ex2(M - now);
+    M = now;
+    L *= old;
+#pragma unroll
+    for (int i = 0; i < kMergeCols; ++i) o[i] *= old;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float wt = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - M);
+      L = fmaf(wt, ml[k].y, L);
+#pragma unroll
+      for (int i = 0; i < kMergeCols / 4; ++i) {
+        o[4 * i] = fmaf(wt, x[k][i].x, o[4 * i]);
+        o[4 * i + 1] = fmaf(wt, x[k][i].y, o[4 * i + 1]);
+        o[4 * i + 2] = fmaf(wt, x[k][i].z, o[4 * i + 2]);
+        o[4 * i + 3] = fmaf(wt, x[k][i].w, o[4 * i + 3]);
+      }
     }
   }
   const float inv = L == 0.f ? 0.f : 1.0f / L;
   const int64_t bh = unit / p.n_rt;
-  const int b = (int)(bh / a.Hkv), h = (int)(bh - (int64_t)b * a.Hkv), qi = R / p.G;
+  const int b = (int)(bh / a.Hkv), h = (int)(bh - (int64_t)b * a.Hkv), qi = p.by_G(R);
   const int64_t qh = ((int64_t)b * a.Lq + qi) * a.Hq + h * p.G + R - qi * p.G;
   uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + qh * 128 + part_col * kMergeCols);
 #pragma unroll
