@@ -28,27 +28,22 @@ SimtPlan simt_plan(int B, int Lq, int Hq, int Hkv, int P, int own) {
   p.n_rt = (Lq * (Hq / Hkv) + ROWS - 1) / ROWS;
   const int64_t base = (int64_t)B * Hkv * p.n_rt;
   const int tiles = (P + KB - 1) / KB + (own ? (Lq + KB - 1) / KB : 0);
-  // two CTAs per SM, at least two key tiles per split
+  // two CTAs per SM as far as there are key tiles
   const int want = (int)((2 * num_sms() + base - 1) / base);
-  p.n_splits = std::max(1, std::min(std::min(want, 32), tiles / 2));
+  p.n_splits = std::max(1, std::min(std::min(want, 32), tiles));
   p.tps = std::max(1, (tiles + p.n_splits - 1) / p.n_splits);
   p.n_splits = std::max(1, (tiles + p.tps - 1) / p.tps);
   return p;
 }
 
-template <typename T> DLLM_DEV void load_vec(const T* p, float* f);   // 16 bytes as fp32
-template <> DLLM_DEV void load_vec<float>(const float* p, float* f) {
+DLLM_DEV void load4(const float* p, float* f) {
   const float4 v = *reinterpret_cast<const float4*>(p);
   f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
 }
-template <> DLLM_DEV void load_vec<__nv_bfloat16>(const __nv_bfloat16* p, float* f) {
-  bf16x8_to_f32(*reinterpret_cast<const uint4*>(p), f);
-}
 
 // ROWS rows of the queries, scaled, into shared memory (pitch d + 4); rows past the last are zero.
-template <typename T>
 DLLM_DEV void load_rows(const Kv8AttnArgs& a, int b, int h, int R0, float mul, float* qs) {
-  constexpr int VE = 16 / (int)sizeof(T);
+  constexpr int VE = 4;
   const int G = a.Hq / a.Hkv, vpr = a.d / VE, pitch = a.d + 4;
   for (int i = threadIdx.x; i < ROWS * vpr; i += 256) {
     const int r = i / vpr, c = (i - r * vpr) * VE, R = R0 + r;
@@ -56,9 +51,10 @@ DLLM_DEV void load_rows(const Kv8AttnArgs& a, int b, int h, int R0, float mul, f
 #pragma unroll
     for (int k = 0; k < VE; ++k) f[k] = 0.f;
     if (R < a.Lq * G)
-      load_vec<T>(static_cast<const T*>(a.q) + (((int64_t)b * a.Lq + R / G) * a.Hq + h * G + R % G) * a.d + c, f);
+      load4(static_cast<const float*>(a.q) + (((int64_t)b * a.Lq + R / G) * a.Hq + h * G + R % G) * a.d + c, f);
 #pragma unroll
-    for (int k = 0; k < VE; ++k) qs[r * pitch + c + k] = f[k] * mul;
+    for (int k = 0; k < VE; k += 4)
+      *reinterpret_cast<float4*>(qs + r * pitch + c + k) = make_float4(f[k] * mul, f[k + 1] * mul, f[k + 2] * mul, f[k + 3] * mul);
   }
 }
 
@@ -69,29 +65,32 @@ DLLM_DEV void load_codes(const uint8_t* codes, const float* scale, int64_t bh, i
   const int64_t runs = (cap + S - 1) / S;
   for (int i = threadIdx.x; i < KB * vpr; i += 256) {
     const int r = i / vpr, c = (i - r * vpr) * 16;
-    float f[16];
+    uint4 u = make_uint4(0, 0, 0, 0);
     float sc = 0.f;
     if (r < nk) {
       sc = scale[bh * runs + (j0 + r) / S];
-      kv8::codes16_to_f32(*reinterpret_cast<const uint4*>(codes + (bh * cap + j0 + r) * (int64_t)d + c), f);
+      u = *reinterpret_cast<const uint4*>(codes + (bh * cap + j0 + r) * (int64_t)d + c);
     }
+    float f[16];
+    kv8::codes16_to_f32(u, f);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) dst[r * pitch + c + k] = r < nk ? f[k] * sc : 0.f;
+    for (int k = 0; k < 16; k += 4)
+      *reinterpret_cast<float4*>(dst + r * pitch + c + k) = make_float4(f[k] * sc, f[k + 1] * sc, f[k + 2] * sc, f[k + 3] * sc);
   }
 }
 
-template <typename T>
-DLLM_DEV void load_own(const T* src, int64_t bh, int cap_own, int d, int j0, int nk, float* dst) {
-  constexpr int VE = 16 / (int)sizeof(T);
+DLLM_DEV void load_own(const float* src, int64_t bh, int cap_own, int d, int j0, int nk, float* dst) {
+  constexpr int VE = 4;
   const int vpr = d / VE, pitch = d + 4;
   for (int i = threadIdx.x; i < KB * vpr; i += 256) {
     const int r = i / vpr, c = (i - r * vpr) * VE;
     float f[VE];
 #pragma unroll
     for (int k = 0; k < VE; ++k) f[k] = 0.f;
-    if (r < nk) load_vec<T>(src + (bh * cap_own + j0 + r) * (int64_t)d + c, f);
+    if (r < nk) load4(src + (bh * cap_own + j0 + r) * (int64_t)d + c, f);
 #pragma unroll
-    for (int k = 0; k < VE; ++k) dst[r * pitch + c + k] = f[k];
+    for (int k = 0; k < VE; k += 4)
+      *reinterpret_cast<float4*>(dst + r * pitch + c + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
   }
 }
 
@@ -114,8 +113,7 @@ DLLM_DEV void scores(const float* qs, const float* ks, int d, int rg, int cg, fl
 
 // One CTA per (b, h, row tile) and key split. Partial results (unnormalised o, m, l per row) go to the workspace when
 // there are several splits.
-template <typename T>
-__global__ void __launch_bounds__(256) attn_kv8_simt_kernel(const Kv8AttnArgs a, SimtPlan p, float* part) {
+__global__ void __launch_bounds__(256, 1) attn_kv8_simt_kernel(const Kv8AttnArgs a, SimtPlan p, float* part) {
   pdl_enter();
   extern __shared__ float sm[];
   const int d = a.d, pitch = d + 4, G = a.Hq / a.Hkv;
@@ -131,7 +129,7 @@ __global__ void __launch_bounds__(256) attn_kv8_simt_kernel(const Kv8AttnArgs a,
   const int64_t bh = (int64_t)b * a.Hkv + h;
   const int len = kv8::prefix_len(a.lens, b, a.P);
   const int R0 = rt * ROWS, n_rows = a.Lq * G;
-  load_rows<T>(a, b, h, R0, a.scale * kLog2e, qs);
+  load_rows(a, b, h, R0, a.scale * kLog2e, qs);
 
   // own keys visible to this thread's rows, and to any row of the tile
   int lim[4];
@@ -162,8 +160,8 @@ __global__ void __launch_bounds__(256) attn_kv8_simt_kernel(const Kv8AttnArgs a,
       load_codes(a.k_codes, a.k_scale, bh, a.cap, a.S, d, j0, nk, ks);
       load_codes(a.v_codes, a.v_scale, bh, a.cap, a.S, d, j0, nk, vs);
     } else {
-      load_own<T>(static_cast<const T*>(a.k_own), bh, a.cap_own, d, j0, nk, ks);
-      load_own<T>(static_cast<const T*>(a.v_own), bh, a.cap_own, d, j0, nk, vs);
+      load_own(static_cast<const float*>(a.k_own), bh, a.cap_own, d, j0, nk, ks);
+      load_own(static_cast<const float*>(a.v_own), bh, a.cap_own, d, j0, nk, vs);
     }
     __syncthreads();
     float s[4][2];
@@ -226,11 +224,11 @@ __global__ void __launch_bounds__(256) attn_kv8_simt_kernel(const Kv8AttnArgs a,
     } else {
       const float inv = l[r] == 0.f ? 0.f : 1.0f / l[r];      // no visible key: zeros; NaN stays
       const int64_t qh = ((int64_t)b * a.Lq + R / G) * a.Hq + h * G + R % G;
-      T* dst = static_cast<T*>(a.out) + qh * d;
+      float* dst = static_cast<float*>(a.out) + qh * d;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        if (c0 < d) dst[c0 + c] = from_f32<T>(o[r][c] * inv);
-        if (c1 < d) dst[c1 + c] = from_f32<T>(o[r][4 + c] * inv);
+        if (c0 < d) dst[c0 + c] = (o[r][c] * inv);
+        if (c1 < d) dst[c1 + c] = (o[r][4 + c] * inv);
       }
       if (cg == 0 && a.lse_out) a.lse_out[qh] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
     }
@@ -238,7 +236,6 @@ __global__ void __launch_bounds__(256) attn_kv8_simt_kernel(const Kv8AttnArgs a,
 }
 
 // One warp per row: the splits' partial results joined by their log-sum-exp, in split order.
-template <typename T>
 __global__ void __launch_bounds__(256) attn_kv8_simt_merge_kernel(const Kv8AttnArgs a, SimtPlan p, const float* part) {
   pdl_enter();
   const int d = a.d, G = a.Hq / a.Hkv, n_rows = a.Lq * G, lane = threadIdx.x & 31;
@@ -265,12 +262,11 @@ __global__ void __launch_bounds__(256) attn_kv8_simt_merge_kernel(const Kv8AttnA
   const int64_t qh = ((int64_t)b * a.Lq + R / G) * a.Hq + h * G + R % G;
 #pragma unroll
   for (int c = 0; c < 4; ++c)
-    if (lane + 32 * c < d) static_cast<T*>(a.out)[qh * d + lane + 32 * c] = from_f32<T>(o[c] * inv);
+    if (lane + 32 * c < d) static_cast<float*>(a.out)[qh * d + lane + 32 * c] = (o[c] * inv);
   if (lane == 0 && a.lse_out) a.lse_out[qh] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // One CTA per (b, h, tile of KB keys): the weights of all rows on its keys, row tile by row tile.
-template <typename T>
 __global__ void __launch_bounds__(256) attn_mass_kv8_simt_kernel(const Kv8AttnArgs a, int n_kt, int n_rt) {
   pdl_enter();
   extern __shared__ float sm[];
@@ -289,7 +285,7 @@ __global__ void __launch_bounds__(256) attn_mass_kv8_simt_kernel(const Kv8AttnAr
   const int n_rows = a.Lq * G;
   for (int rt = 0; rt < n_rt; ++rt) {
     __syncthreads();
-    load_rows<T>(a, b, h, rt * ROWS, a.scale * kLog2e, qs);
+    load_rows(a, b, h, rt * ROWS, a.scale * kLog2e, qs);
     __syncthreads();
     float s[4][2];
     scores(qs, ks, d, rg, cg, s);
@@ -324,40 +320,29 @@ size_t attn_kv8_simt_workspace_bytes(int B, int Lq, int Hq, int Hkv, int d, int 
   return (size_t)B * Hkv * p.n_rt * p.n_splits * ROWS * (d + 4) * 4;
 }
 
-template <typename T>
-static int run_simt(const Kv8AttnArgs& a, cudaStream_t s) {
+int launch_attn_kv8_simt(const Kv8AttnArgs& a, cudaStream_t s) {
   const SimtPlan p = simt_plan(a.B, a.Lq, a.Hq, a.Hkv, a.P, a.k_own != nullptr);
   const size_t smem = ((size_t)(ROWS + 2 * KB) * (a.d + 4) + ROWS * PD) * 4;
-  const int st = set_max_smem<attn_kv8_simt_kernel<T>>(((ROWS + 2 * KB) * 132 + ROWS * PD) * 4);
+  const int st = set_max_smem<attn_kv8_simt_kernel>(((ROWS + 2 * KB) * 132 + ROWS * PD) * 4);
   if (st) return st;
   float* part = static_cast<float*>(a.ws);
-  launch_pdl(attn_kv8_simt_kernel<T>, dim3((unsigned)(a.B * a.Hkv * p.n_rt), p.n_splits), 256, smem, s, a, p, part);
+  launch_pdl(attn_kv8_simt_kernel, dim3((unsigned)(a.B * a.Hkv * p.n_rt), p.n_splits), 256, smem, s, a, p, part);
   DLLM_CHECK_LAUNCH("attn_kv8_simt_kernel");
   if (p.n_splits > 1) {
     const int64_t rows = (int64_t)a.B * a.Lq * a.Hq;
-    launch_pdl(attn_kv8_simt_merge_kernel<T>, (unsigned)((rows + 7) / 8), 256, 0, s, a, p, (const float*)part);
+    launch_pdl(attn_kv8_simt_merge_kernel, (unsigned)((rows + 7) / 8), 256, 0, s, a, p, (const float*)part);
     DLLM_CHECK_LAUNCH("attn_kv8_simt_merge_kernel");
   }
   return DLLM_OK;
-}
-
-int launch_attn_kv8_simt(const Kv8AttnArgs& a, cudaStream_t s) {
-  return a.dtype == DLLM_BF16 ? run_simt<__nv_bfloat16>(a, s) : run_simt<float>(a, s);
 }
 
 int launch_attn_mass_kv8_simt(const Kv8AttnArgs& a, cudaStream_t s) {
   const int n_kt = (a.P + KB - 1) / KB, n_rt = (a.Lq * (a.Hq / a.Hkv) + ROWS - 1) / ROWS;
   const size_t smem = ((size_t)(ROWS + KB) * (a.d + 4) + 16 * KB) * 4;
   const unsigned grid = (unsigned)((int64_t)a.B * a.Hkv * n_kt);
-  if (a.dtype == DLLM_BF16) {
-    const int st = set_max_smem<attn_mass_kv8_simt_kernel<__nv_bfloat16>>(((ROWS + KB) * 132 + 16 * KB) * 4);
-    if (st) return st;
-    launch_pdl(attn_mass_kv8_simt_kernel<__nv_bfloat16>, grid, 256, smem, s, a, n_kt, n_rt);
-  } else {
-    const int st = set_max_smem<attn_mass_kv8_simt_kernel<float>>(((ROWS + KB) * 132 + 16 * KB) * 4);
-    if (st) return st;
-    launch_pdl(attn_mass_kv8_simt_kernel<float>, grid, 256, smem, s, a, n_kt, n_rt);
-  }
+  const int st = set_max_smem<attn_mass_kv8_simt_kernel>(((ROWS + KB) * 132 + 16 * KB) * 4);
+  if (st) return st;
+  launch_pdl(attn_mass_kv8_simt_kernel, grid, 256, smem, s, a, n_kt, n_rt);
   DLLM_CHECK_LAUNCH("attn_mass_kv8_simt_kernel");
   return DLLM_OK;
 }

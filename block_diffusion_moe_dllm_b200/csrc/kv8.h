@@ -62,7 +62,7 @@ int launch_attn_mass_kv8(const Kv8AttnArgs& a, cudaStream_t s);
 size_t attn_kv8_tc_workspace_bytes(int B, int Lq, int Hq, int Hkv);
 int launch_attn_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s);
 int launch_attn_mass_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s);
-// SIMT variants (any storage type)
+// SIMT variants (fp32)
 size_t attn_kv8_simt_workspace_bytes(int B, int Lq, int Hq, int Hkv, int d, int P, int own);
 int launch_attn_kv8_simt(const Kv8AttnArgs& a, cudaStream_t s);
 int launch_attn_mass_kv8_simt(const Kv8AttnArgs& a, cudaStream_t s);

@@ -1,7 +1,7 @@
 """Per-kernel timing of the library's main calls at a workload's shapes (CUDA events, kernels launched alone).
 
     python -m block_diffusion_moe_dllm_b200.kernel_bench [--kernel lm_head|proj|experts|expert_gemms|unmask|attn|
-                                                          route|all|step]
+                                                          kv8|route|all|step]
                                                          [--workload NAME] [--reps N]
 
 Each line reports the mean time of one call, its algorithmic bytes (weights and activations it must move at
@@ -326,6 +326,42 @@ def trace_block(eng, tokens, mask):
             for k, v in sorted(rows.items(), key=lambda kv: -kv[1][1])]
 
 
+def bench_kv8(w: Workload, reps, dev, stream, S=32):
+    """The 8-bit KV cache calls around one block: the prefix stored, the block's attention over it, the weights it puts on
+    the prefix, and the prefix evicted to half (first 4 and last 128 positions kept)."""
+    B, Hkv, d, P, L, Hq = w.B, w.Hkv, w.d, w.P, w.L, w.Hq
+    keep, runs = max(P // 2, min(P, 132)), -(-P // S)
+    k, v = (synth.normal((B, Hkv, P, d), 1.0, 6, x, dev) for x in ("kb8_k", "kb8_v"))
+    ko, vo = (synth.normal((B, Hkv, L, d), 1.0, 6, x, dev) for x in ("kb8_ko", "kb8_vo"))
+    q = synth.normal((B, L, Hq, d), 1.0, 6, "kb8_q", dev)
+    codes = [torch.zeros((B, Hkv, n, d), dtype=torch.uint8, device=dev) for n in (P, P, keep, keep)]
+    scale = [torch.ones((B, Hkv, n), device=dev) for n in (runs, runs, -(-keep // S), -(-keep // S))]
+    out = torch.empty((B, L, Hq * d), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((B, L, Hq), device=dev)
+    mass, mass2 = torch.zeros((B, Hkv, P), device=dev), torch.zeros((B, Hkv, keep), device=dev)
+    pos = torch.zeros((B, 1, keep), dtype=torch.int32, device=dev)
+    lens = torch.zeros(B, dtype=torch.int32, device=dev)
+    ws = bd.Workspace(64 << 20, dev)
+    cached = B * Hkv * P * (d + 4 / S)
+    calls = [
+        ("kv8_store", lambda: bd.kv8_store(k, v, *codes[:2], *scale[:2], B, Hkv, d, P, P, P, S, bd.BF16),
+         2 * cached + 4 * B * Hkv * P * d, 0.0),
+        ("block_attn_kv8", lambda: bd.block_attn_kv8(q, *codes[:2], *scale[:2], out, B, L, Hq, Hkv, d, P, P, S, L, bd.BF16,
+                                                     k_own=ko, v_own=vo, cap_own=L, lse=lse, ws=ws),
+         2 * cached + B * L * d * 2 * (2 * Hq + 2 * Hkv), 4.0 * B * L * Hq * (P + L) * d),
+        ("attn_mass_kv8", lambda: bd.attn_mass_kv8(q, codes[0], scale[0], lse, mass, mass, B, L, Hq, Hkv, d, P, P, S,
+                                                   bd.BF16, ws=ws),
+         cached + B * L * Hq * d * 2 + 8 * B * Hkv * P, 2.0 * B * L * Hq * P * d),
+        ("kv8_evict", lambda: bd.kv8_evict(*codes[:2], *scale[:2], mass, *codes[2:], *scale[2:], mass2, pos, lens, B, Hkv, d,
+                                           P, P, keep, keep, S, min(4, keep), min(128, keep - min(4, keep)), ws=ws),
+         4 * B * Hkv * P + 4 * B * Hkv * keep * (d + 4 / S), 0.0)]
+    res = []
+    for name, call, nbytes, flops in calls:
+        t = timed(call, reps, stream)
+        res.append(_result(name, t, nbytes, _flops({"prefix": P, "rows": B * L}, flops, t) if flops else None))
+    return res
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--kernel", default="all")
@@ -353,6 +389,8 @@ def main():
         out.append(bench_unmask(w, a.reps, dev, stream))
     if a.kernel in ("attn", "all"):
         out.append(bench_attn(w, a.reps, dev, stream))
+    if a.kernel in ("kv8", "all") and w.P > 0 and w.dtype == "bf16":
+        out.extend(bench_kv8(w, a.reps, dev, stream))
     if a.kernel == "step":
         out.append(bench_step(w, a.reps, dev, stream))
     if a.kernel == "block":

@@ -445,6 +445,83 @@ def test_serving_run():
         assert torch.equal(x, y)
 
 
+def _calls(q, kc, vc, ks, vs, ko, vo, lens, B, Lq, Hq, Hkv, d, P, S, keep, ws):
+    """Outputs of the attention, the weights and an eviction, and a function that makes the three calls."""
+    out = torch.zeros((B, Lq, Hq * d), dtype=q.dtype, device=DEV)
+    lse, mass = torch.zeros((B, Lq, Hq), device=DEV), torch.zeros((B, Hkv, P), device=DEV)
+    c2 = [torch.zeros((B, Hkv, keep, d), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    s2 = [torch.ones((B, Hkv, cdiv(keep, S)), device=DEV) for _ in range(2)]
+    m2 = torch.zeros((B, Hkv, keep), device=DEV)
+    pos, l2 = torch.zeros((B, Hkv, keep), dtype=torch.int32, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    dt = bd.BF16 if q.dtype == torch.bfloat16 else bd.F32
+
+    def run(stream=None):
+        bd.block_attn_kv8(q, kc, vc, ks, vs, out, B, Lq, Hq, Hkv, d, P, P, S, Lq, dt, prefix_len=lens, k_own=ko, v_own=vo,
+                          cap_own=Lq + 3, lse=lse, ws=ws, stream=stream)
+        bd.attn_mass_kv8(q, kc, ks, lse, None, mass, B, Lq, Hq, Hkv, d, P, P, S, dt, prefix_len=lens, ws=ws, stream=stream)
+        bd.kv8_evict(kc, vc, ks, vs, mass, *c2, *s2, m2, pos, l2, B, Hkv, d, P, P, keep, keep, S, 2, 3, 1, prefix_len=lens,
+                     ws=ws, stream=stream)
+    return [out, lse, mass, *c2, *s2, m2, pos, l2], run
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_graph_replay_follows_the_device_lengths(dtype, d):
+    """Lengths are read when the kernels run: one captured graph serves other lengths, zero among them, and gives the bits
+    of direct calls."""
+    B, Lq, Hq, Hkv, P, S, keep = 5, 16, 8, 2, 900, 32, 200
+    q, kc, vc, ks, vs, _, _, ko, vo = attn_inputs(dtype, B, Lq, Hq, Hkv, d, P, S, None, True, 61)
+    lens = torch.full((B,), P, dtype=torch.int32, device=DEV)
+    ws = bd.Workspace(64 << 20, DEV)
+    outs, run = _calls(q, kc, vc, ks, vs, ko, vo, lens, B, Lq, Hq, Hkv, d, P, S, keep, ws)
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for new in ((900, 0, 1, 128, 777), (5, 6, 0, 0, 0), (900, 899, 898, 640, 129)):
+        lens.copy_(torch.tensor(new, dtype=torch.int32))
+        for x in outs:
+            x.zero_()
+        graph.replay()
+        got = [x.clone() for x in outs]
+        for x in outs:
+            x.zero_()
+        run()
+        for x, y in zip(got, outs):
+            assert torch.equal(x, y)
+        assert outs[-1].tolist() == [min(n, keep) for n in new]
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    """Calls that overlap on two streams, each with its own workspace, give the bits they give alone."""
+    B, Lq, Hq, Hkv, d, P, S, keep = 4, 32, 16, 4, 128, 2000, 32, 500
+    sides, alone = [], []
+    for seed in (71, 72):
+        q, kc, vc, ks, vs, _, _, ko, vo = attn_inputs("bf16", B, Lq, Hq, Hkv, d, P, S, None, True, seed)
+        lens = torch.tensor([P, P - 300 * (seed - 70), 1, 1500], dtype=torch.int32, device=DEV)
+        sides.append(_calls(q, kc, vc, ks, vs, ko, vo, lens, B, Lq, Hq, Hkv, d, P, S, keep, bd.Workspace(64 << 20, DEV)))
+        sides[-1][1]()
+        torch.cuda.synchronize()
+        alone.append([x.clone() for x in sides[-1][0]])
+    streams = [torch.cuda.Stream() for _ in sides]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (outs, run), st in zip(sides, streams):
+            run(st)
+    torch.cuda.synchronize()
+    for (outs, _), want in zip(sides, alone):
+        for x, y in zip(outs, want):
+            assert torch.equal(x, y)
+
+
+def test_tensors_off_the_current_device_are_refused():
+    x = torch.zeros((1, 1, 16, 128), dtype=torch.bfloat16)
+    c = torch.zeros((1, 1, 16, 128), dtype=torch.uint8)
+    s = torch.zeros((1, 1, 1))
+    with pytest.raises(bd.DllmError) as e:
+        bd.kv8_store(x, x, c, c, s, s, 1, 1, 128, 16, 16, 16, 16, bd.BF16)
+    assert e.value.code == bd.ERR_INVALID_ARG
+
+
 def test_long_cache_offsets():
     """More than 2^31 code bytes in one tensor: the last row's keys and values are the ones read, stored and moved."""
     B, Hkv, d, S, cap = 5, 4, 128, 128, 900_000
