@@ -655,9 +655,9 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       }
       for (int t = w.ta; t < w.end(); ++t) {
         uint8_t* dst = sW + g * VTILE;
-        wait_for(&bar.w_empty[g], wph, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
         if (t < w.tp) {
           const int n = min(KT, w.len - t * KT);
+          wait_for(&bar.w_empty[g], wph, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
           wait_for(&bar.v_full[v], vph, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
           // Eight neighbouring lanes take the same 16 columns of eight neighbouring keys: with the 128-byte swizzle on both
           // sides their 16-byte pieces fall on different banks, and every address is a lane's own plus a constant.
@@ -692,13 +692,15 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           const int64_t at = (bh * a.cap_own + j0) * 128 + 32 * (ct & 3);
           // largest finite magnitudes (a row with an infinity or NaN counts as 0: K makes all its codes NaN)
           uint32_t mk = 0, mv = 0;
-#pragma unroll 1
+          auto load_own = [&](int r, Quarter& k8, Quarter& v8) {
+            k8.load(r < n ? static_cast<const __nv_bfloat16*>(a.k_own) + at + r * 128 : nullptr);
+            v8.load(r < n ? static_cast<const __nv_bfloat16*>(a.v_own) + at + r * 128 : nullptr);
+          };
+#pragma unroll 2
           for (int r = ct >> 2; r < KT; r += 32) {
-            Quarter q;
-            q.load(r < n ? static_cast<const __nv_bfloat16*>(a.k_own) + at + r * 128 : nullptr);
-            const uint32_t x = q.amax();
-            q.load(r < n ? static_cast<const __nv_bfloat16*>(a.v_own) + at + r * 128 : nullptr);
-            const uint32_t y = q.amax();
+            Quarter k8, v8;
+            load_own(r, k8, v8);
+            const uint32_t x = k8.amax(), y = v8.amax();
             mk = max(mk, x < kInfBits ? x : 0u);
             mv = max(mv, y < kInfBits ? y : 0u);
           }
@@ -711,6 +713,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           tc::named_bar_sync(kBarConv, 128);
           const int ek = bits_exp(max(max(bar.red[0][0], bar.red[0][1]), max(bar.red[0][2], bar.red[0][3])));
           const int ev = bits_exp(max(max(bar.red[1][0], bar.red[1][1]), max(bar.red[1][2], bar.red[1][3])));
+          wait_for(&bar.w_empty[g], wph, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
           if (ct == 0) bar.run_own[g] = make_float4(kv8::exp2i(ek), (float)ev, kv8::exp2i(-ev), 0.f);
           const uint32_t k0 = k, k1 = parts == 2 ? (k + 1) % NK : k;
           for (int i = 0; i < parts; ++i) {
@@ -721,14 +724,13 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           const float ik = kv8::exp2i(-ek), iv = kv8::exp2i(-ev);
 #pragma unroll 1
           for (int r = ct >> 2; r < KT; r += 32) {
-            Quarter q;
-            q.load(r < n ? static_cast<const __nv_bfloat16*>(a.k_own) + at + r * 128 : nullptr);
-            q.split(q.amax() < kInfBits ? ik : qnan(), r, ct & 3, sK + k0 * KSTAGE, sK + k1 * KSTAGE);
-            q.load(r < n ? static_cast<const __nv_bfloat16*>(a.v_own) + at + r * 128 : nullptr);
+            Quarter k8, v8;
+            load_own(r, k8, v8);
+            k8.split(k8.amax() < kInfBits ? ik : qnan(), r, ct & 3, sK + k0 * KSTAGE, sK + k1 * KSTAGE);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float f[8];
-              bf16x8_to_f32(q.raw[i], f);
+              bf16x8_to_f32(v8.raw[i], f);
               const int gr = 4 * (ct & 3) + i;      // granule of 8 values: chunk gr >> 3
               *reinterpret_cast<uint4*>(dst + (gr >> 3) * VCHUNK + r * 128 + (((gr & 7) ^ (r & 7)) << 4)) =
                   make_uint4(f16x2(f[0] * iv, f[1] * iv), f16x2(f[2] * iv, f[3] * iv), f16x2(f[4] * iv, f[5] * iv),
@@ -991,8 +993,11 @@ __global__ void __launch_bounds__(KT) attn_kv8_merge_kernel(const __grid_constan
 // the thread's own; lse2 comes from shared memory. Key tiles are dealt to the CTAs like the attention's; a CTA goes over
 // its tiles of a (b, kv head) once per row tile of the queries (more than one: K comes from L2 after the first time).
 // Bound by the exponentials: 128 x 128 per key tile and row tile, 1024 clocks, against 512 of MMAs and 710 of HBM.
-// Roles: warp 0 TMA, warp 1 MMA, warps 4-7 and 8-11 alternate key tiles, warps 12-15 stage the queries.
-constexpr int MK = 5, MS = 4;              // stages of the K ring, S buffers
+// Roles: warp 0 TMA, warp 1 MMA, warps 4-15 three groups that take the key tiles in turn, each with an S buffer (a thread's
+// loads, exponentials and sums follow one another, so two groups left the special-function units half idle: 4 rows of
+// 32768 keys, 128 rows a kv head, 35.3 us with two, 31.0 with three, 30.5 with four), warps 16-19 stage the queries.
+constexpr int MK = 5, MS = 3;              // stages of the K ring, S buffers = groups
+constexpr int MASS_NT = 128 * (2 + MS);
 struct MassBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[MK], k_empty[MK];
@@ -1009,7 +1014,7 @@ constexpr int MASS_SMEM = 1024 + 2 * 2 * KSTAGE /*Q*/ + MK * KSTAGE + (int)sizeo
 static_assert(MASS_SMEM <= 232448, "shared memory budget");
 static_assert(MASS_SMEM > 233472 / 2, "tensor-memory kernels must not share an SM");
 
-__global__ void __launch_bounds__(NT, 1)
+__global__ void __launch_bounds__(MASS_NT, 1)
 attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ Params p, int q_rt) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1023,7 +1028,7 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
     bar.abort_flag = 0;
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bar.q_full[i], 4);
-      tc::mbar_init(&bar.q_empty[i], 1 + 8);
+      tc::mbar_init(&bar.q_empty[i], 1 + 4 * MS);
     }
     for (int i = 0; i < MK; ++i) {
       tc::mbar_init(&bar.k_full[i], 1);
@@ -1120,10 +1125,10 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
       tc::mma_commit(&bar.done);
       tc::mbar_wait(&bar.done, 0, 1u << 20);
     }
-  } else if (warp >= 12) {
+  } else if (warp >= 4 + 4 * MS) {
     // ------------------------------------------------------------------ queries: four threads per row, 32 rows at a time
-    const int ct = tid - 384;
-    const uint32_t cw = warp - 12;
+    const int ct = tid - 128 * (1 + MS);
+    const uint32_t cw = warp - 4 - 4 * MS;
     uint32_t seg = 0;
     for (; w.n > 0; w.next(p))
       for (int rt = 0; rt < q_rt; ++rt, ++seg) {
@@ -1176,10 +1181,10 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
         const int cols = min(KT, p.n_rows - rt * KT);
         wait_for(&bar.q_full[qb], (seg >> 1) & 1, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
         const float f = bar.factor[qb];
-        // the other group may have added the last row tile to this group's tiles
-        if (rt > 0) tc::named_bar_sync(kBarPair, 256);
+        // another group may have added the last row tile to this group's tiles
+        if (rt > 0) tc::named_bar_sync(kBarPair, 128 * MS);
         for (int t = w.ta; t < t_end; ++t, ++it) {
-          if ((int)(it & 1) == grp) {
+          if ((int)(it % MS) == grp) {
             const int key = t * KT + row;
             const bool live = key < w.len;
             float ks = 0.f, old = 0.f;
@@ -1324,7 +1329,7 @@ int launch_attn_mass_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
   if (st) return st;
   st = set_max_smem<attn_mass_kv8_tc_kernel>(MASS_SMEM);
   if (st) return st;
-  launch_pdl(attn_mass_kv8_tc_kernel, p.n_cta, NT, MASS_SMEM, s, mk, p, (p.n_rows + KT - 1) / KT);
+  launch_pdl(attn_mass_kv8_tc_kernel, p.n_cta, MASS_NT, MASS_SMEM, s, mk, p, (p.n_rows + KT - 1) / KT);
   DLLM_CHECK_LAUNCH("attn_mass_kv8_tc_kernel");
   return DLLM_OK;
 }
