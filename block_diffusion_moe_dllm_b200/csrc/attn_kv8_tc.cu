@@ -697,7 +697,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             v8.load(r < n ? static_cast<const __nv_bfloat16*>(a.v_own) + at + r * 128 : nullptr);
           };
 #pragma unroll 2
-          for (int r = ct >> 2; r < KT; r += 32) {
+          for (int r = ct >> 2; r - (ct >> 2) < n; r += 32) {
             Quarter k8, v8;
             load_own(r, k8, v8);
             const uint32_t x = k8.amax(), y = v8.amax();
@@ -724,17 +724,24 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           const float ik = kv8::exp2i(-ek), iv = kv8::exp2i(-ev);
 #pragma unroll 1
           for (int r = ct >> 2; r < KT; r += 32) {
+            // rows past the last: V has to be zeros (their weight is 0), K may be anything (their scores are masked)
+            const bool zero = r - (ct >> 2) >= n;
             Quarter k8, v8;
-            load_own(r, k8, v8);
-            k8.split(k8.amax() < kInfBits ? ik : qnan(), r, ct & 3, sK + k0 * KSTAGE, sK + k1 * KSTAGE);
+            if (!zero) {
+              load_own(r, k8, v8);
+              k8.split(k8.amax() < kInfBits ? ik : qnan(), r, ct & 3, sK + k0 * KSTAGE, sK + k1 * KSTAGE);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float f[8];
-              bf16x8_to_f32(v8.raw[i], f);
               const int gr = 4 * (ct & 3) + i;      // granule of 8 values: chunk gr >> 3
-              *reinterpret_cast<uint4*>(dst + (gr >> 3) * VCHUNK + r * 128 + (((gr & 7) ^ (r & 7)) << 4)) =
-                  make_uint4(f16x2(f[0] * iv, f[1] * iv), f16x2(f[2] * iv, f[3] * iv), f16x2(f[4] * iv, f[5] * iv),
-                             f16x2(f[6] * iv, f[7] * iv));
+              uint4 x = make_uint4(0, 0, 0, 0);
+              if (!zero) {
+                float f[8];
+                bf16x8_to_f32(v8.raw[i], f);
+                x = make_uint4(f16x2(f[0] * iv, f[1] * iv), f16x2(f[2] * iv, f[3] * iv), f16x2(f[4] * iv, f[5] * iv),
+                               f16x2(f[6] * iv, f[7] * iv));
+              }
+              *reinterpret_cast<uint4*>(dst + (gr >> 3) * VCHUNK + r * 128 + (((gr & 7) ^ (r & 7)) << 4)) = x;
             }
           }
           fence_async_smem();
