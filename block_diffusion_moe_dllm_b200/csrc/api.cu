@@ -574,6 +574,15 @@ int dllm_kv8_store(const dllm_kv8_store_desc* d, const void* k, const void* v, c
       "kv8_store: too many rows for one call");
   REQ(aligned16(k) && aligned16(v) && aligned16(k_codes) && aligned16(v_codes), DLLM_ERR_ALIGN,
       "kv8_store: k, v and the code tensors must be 16-byte aligned");
+  {
+    const size_t bh = (size_t)d->B * d->Hkv, src = bh * d->cap_src * d->d * esize(d->dtype), cb = bh * d->cap * d->d,
+                 sb = bh * ((d->cap + d->scale_len - 1) / d->scale_len) * 4;
+    const void* p[6] = {k, v, k_codes, v_codes, k_scale, v_scale};      // k and v may be the same
+    const size_t n[6] = {src, src, cb, cb, sb, sb};
+    for (int i = 0; i < 6; ++i)
+      for (int j = std::max(i + 1, 2); j < 6; ++j)
+        REQ(!overlaps(p[i], n[i], p[j], n[j]), DLLM_ERR_INVALID_ARG, "kv8_store: an output overlaps another array");
+  }
   if (d->n == 0) return DLLM_OK;
   Kv8StoreArgs a;
   a.B = d->B; a.Hkv = d->Hkv; a.d = d->d; a.n = d->n; a.cap_src = d->cap_src; a.src_row = d->src_row; a.cap = d->cap;
@@ -679,7 +688,8 @@ int dllm_kv8_evict(const dllm_kv8_evict_desc* d, const void* k_codes, const void
     const size_t nout[7] = {co, co, so, so, bh * d->cap_out * 4, hs * d->cap_out * 4, (size_t)d->B * 4};
     for (int i = 0; i < 7; ++i)
       for (int j = 0; j < 7; ++j)
-        REQ(!overlaps(in[i], nin[i], out[j], nout[j]), DLLM_ERR_INVALID_ARG, "kv8_evict: an output overlaps an input");
+        REQ(!overlaps(in[i], nin[i], out[j], nout[j]) && (j <= i || !overlaps(out[i], nout[i], out[j], nout[j])),
+            DLLM_ERR_INVALID_ARG, "kv8_evict: an output overlaps another array");
   }
   st = check_ws(ws, ws_bytes, dllm_kv8_evict_workspace_size(d));
   if (st) return st;

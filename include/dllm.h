@@ -453,7 +453,7 @@ DLLM_API int dllm_denoise_step_views(const dllm_model* model, const dllm_state* 
  * dllm_kv8_store quantises n rows of K and V of every (row, kv head) into it. The scale of a run is 2^k, k the least
  * integer for which its largest finite magnitude is at most 448 * 2^k, limited to -64 <= k <= 120; every value is
  * divided by it (exactly) and rounded once to E4M3, nearest even. Infinities become +-448 times the scale, NaN stays
- * NaN.
+ * NaN. No output overlaps another array.
  *   k, v      [B, Hkv, cap_src, d] in the storage type, 16-byte aligned; token t is row src_row + t
  *   src_pos   [B, pos_stride] int32 (nullable): token t of batch row b is source row src_pos[b, t] instead (a position
  *             list as dllm_prefix_retain writes it); positions outside [0, cap_src) are stored as zeros
@@ -483,7 +483,8 @@ DLLM_API int dllm_kv8_store(const dllm_kv8_store_desc* desc, const void* k, cons
  *   out          [B, Lq, Hq * d], 16-byte aligned; zeros where a query sees no key
  *   lse          [B, Lq, Hq] fp32 (nullable): log of the sum of exp(score) over the query's keys, -inf without keys
  * scale <= 0 selects 1/sqrt(d). Any Hq a multiple of Hkv. bf16: d == 128. Own V rows must be finite (a query's weight
- * on a row it does not see is 0, and 0 times infinity is not); V scales below 2^-64 are read as 2^-64.
+ * on a row it does not see is 0, and 0 times infinity is not). bf16 reads V scales below 2^-64 as 2^-64 and holds the
+ * weights in f16 (11 bits; those below 2^-27 of the row's largest so far count as 0), their sums in fp32.
  */
 typedef struct {
   int32_t B, Lq, Hq, Hkv, d;
@@ -534,7 +535,7 @@ DLLM_API size_t dllm_attn_mass_kv8_workspace_size(const dllm_attn_mass_desc* des
  *   pos       [B, per_head ? Hkv : 1, cap] int32 (nullable): the rows' positions, their row numbers without it
  *   k_out, v_out [B, Hkv, cap_out, d]; k_scale_out, v_scale_out [B, Hkv, ceil(cap_out / scale_len)]; mass_out [B, Hkv,
  *   cap_out]; keep_pos [B, per_head ? Hkv : 1, cap_out] int32: the kept rows' positions; len_out [B] int32.
- * Rows past len_out are left as they were. No output overlaps an input. n_first + n_last <= n_keep <= cap_out.
+ * Rows past len_out are left as they were. No output overlaps another array. n_first + n_last <= n_keep <= cap_out.
  */
 typedef struct {
   int32_t B, Hkv, d;

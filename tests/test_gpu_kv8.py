@@ -355,6 +355,25 @@ def test_kv8_evict(B, Hkv, d, P, S, keep, first, last, lens, per_head, ties):
                 assert torch.all(dst[b, h, c:] == 0x33) and torch.all(sd[b, h, len(wn):] == -1)
 
 
+def test_empty_calls():
+    """No rows to store, no prefix to attend to, to weigh or to evict: nothing is written but zeros for the queries."""
+    B, Hkv, d, S = 2, 2, 128, 16
+    c = [torch.full((B, Hkv, 16, d), 7, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    s = [torch.full((B, Hkv, 1), 7.0, device=DEV) for _ in range(4)]
+    x = torch.zeros((B, Hkv, 16, d), dtype=torch.bfloat16, device=DEV)
+    bd.kv8_store(x, x, c[0], c[1], s[0], s[1], B, Hkv, d, 0, 16, 16, S, bd.BF16)
+    q = synth.normal((B, 3, 4, d), 1.0, 91, "q", DEV)
+    out, lse = torch.full((B, 3, 4 * d), 5.0, dtype=torch.bfloat16, device=DEV), torch.zeros((B, 3, 4), device=DEV)
+    bd.block_attn_kv8(q, c[0], c[1], s[0], s[1], out, B, 3, 4, Hkv, d, 0, 16, S, 1, bd.BF16, lse=lse)
+    assert not out.any() and torch.all(lse == -float("inf"))
+    mass, m2 = torch.full((B, Hkv, 16), 3.0, device=DEV), torch.full((B, Hkv, 16), 3.0, device=DEV)
+    bd.attn_mass_kv8(q, c[0], s[0], lse, None, mass, B, 3, 4, Hkv, d, 0, 16, S, bd.BF16)
+    pos, lens = torch.full((B, 1, 16), 9, dtype=torch.int32, device=DEV), torch.full((B,), 9, dtype=torch.int32, device=DEV)
+    bd.kv8_evict(c[0], c[1], s[0], s[1], mass, c[2], c[3], s[2], s[3], m2, pos, lens, B, Hkv, d, 0, 16, 4, 16, S)
+    assert lens.tolist() == [0, 0] and torch.all(pos == 9)
+    assert all(torch.all(y == 7) for y in c + s) and torch.all(mass == 3) and torch.all(m2 == 3)
+
+
 # ------------------------------------------------------------------------------------------------ together
 def test_serving_run():
     """A prompt stored, a block attending over it, its weights accumulated, the prefix evicted to half, the block's own

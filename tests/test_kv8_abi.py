@@ -23,12 +23,13 @@ def lib():
 
 
 # ------------------------------------------------------------------------------------------------ refusals
-def _store(lib, src_pos=None, dst_rows=None, k=FAKE, codes=FAKE, **kw):
+def _store(lib, src_pos=None, dst_rows=None, k=FAKE, codes=1 << 41, vc=5 << 40, **kw):
     f = dict(B=2, Hkv=4, d=128, n=32, cap_src=64, src_row=0, cap=96, dst_row=32, scale_len=32, dtype=bd.BF16,
              pos_stride=32)
     f.update(kw)
     d = bd.Kv8StoreDesc(**f)
-    return lib.dllm_kv8_store(C.byref(d), k, FAKE, src_pos, dst_rows, codes, FAKE, FAKE, FAKE, None)
+    # arrays far enough apart; codes is the first output
+    return lib.dllm_kv8_store(C.byref(d), k, 1 << 40, src_pos, dst_rows, codes, vc, 3 << 40, 4 << 40, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -38,8 +39,8 @@ def _store(lib, src_pos=None, dst_rows=None, k=FAKE, codes=FAKE, **kw):
     (dict(scale_len=48), bd.ERR_UNSUPPORTED), (dict(scale_len=0), bd.ERR_UNSUPPORTED),
     (dict(src_row=33), bd.ERR_SHAPE), (dict(src_row=-1), bd.ERR_SHAPE), (dict(dst_row=16), bd.ERR_SHAPE),
     (dict(dst_row=96), bd.ERR_SHAPE), (dict(dst_row=-32), bd.ERR_SHAPE), (dict(src_pos=FAKE, pos_stride=31), bd.ERR_SHAPE),
-    (dict(k=FAKE + 2), bd.ERR_ALIGN), (dict(codes=FAKE + 8), bd.ERR_ALIGN),
-    (dict(B=1 << 20, Hkv=1 << 12), bd.ERR_UNSUPPORTED)])
+    (dict(k=FAKE + 2), bd.ERR_ALIGN), (dict(codes=FAKE + 8), bd.ERR_ALIGN), (dict(codes=FAKE), bd.ERR_INVALID_ARG),
+    (dict(vc=1 << 41), bd.ERR_INVALID_ARG), (dict(B=1 << 20, Hkv=1 << 12), bd.ERR_UNSUPPORTED)])
 def test_store_refuses(lib, kw, code):
     assert _store(lib, **kw) == code
     assert "kv8_store" in lib.dllm_last_error().decode()
@@ -97,6 +98,7 @@ def _evict(lib, ptrs=None, ws=FAKE, pos=None, **kw):
     (dict(ptrs={0: None}), bd.ERR_INVALID_ARG), (dict(ptrs={11: None}), bd.ERR_INVALID_ARG),
     (dict(ptrs={5: 1 << 24}), bd.ERR_INVALID_ARG),                      # in place: k_out on k_codes
     (dict(ptrs={9: (5 << 24) + 256}), bd.ERR_INVALID_ARG),              # mass_out inside mass
+    (dict(ptrs={6: 6 << 24}), bd.ERR_INVALID_ARG),                      # v_out on k_out
     (dict(n_keep=0), bd.ERR_SHAPE), (dict(n_keep=65), bd.ERR_SHAPE), (dict(n_first=50, n_last=15), bd.ERR_INVALID_ARG),
     (dict(n_first=-1), bd.ERR_INVALID_ARG), (dict(cap=100), bd.ERR_SHAPE), (dict(scale_len=20), bd.ERR_UNSUPPORTED),
     (dict(d=100), bd.ERR_UNSUPPORTED), (dict(ptrs={6: (7 << 24) + 8}), bd.ERR_ALIGN), (dict(ws=None), bd.ERR_WORKSPACE)])
