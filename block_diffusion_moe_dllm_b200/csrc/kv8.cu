@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv8_select_kernel(const Kv8Evi
     double t[kFlight];
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) t[k] = 0.0;
+#pragma unroll 4
     for (int g = 0; g < heads; ++g) {        // summed in 64 bits, in head order
       float f[kFlight];
 #pragma unroll
