@@ -39,15 +39,19 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
   const int nvec = ok ? rows * vpr : 0;
   const T* src = static_cast<const T*>(is_v ? a.v : a.k) + bh * (int64_t)a.cap_src * a.d;
   uint4 vec[VPT];
+  // without a position list the run's source rows are contiguous, and so are its vectors
+  const T* run_src = src + ((int64_t)a.src_row + t0) * a.d;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int id = gt + i * TG;
     vec[i] = make_uint4(0, 0, 0, 0);
     if (id < nvec) {
-      const int r = id / vpr, c = id - r * vpr;
-      int row = a.src_row + t0 + r;
-      if (a.src_pos) row = a.src_pos[(int64_t)b * a.pos_stride + t0 + r];
-      if (row >= 0 && row < a.cap_src) vec[i] = ld_nc_v4(src + (int64_t)row * a.d + (int64_t)c * VE);
+      if (!a.src_pos) {
+        vec[i] = ld_nc_v4(run_src + id * VE);
+      } else {
+        const int r = id / vpr, row = a.src_pos[(int64_t)b * a.pos_stride + t0 + r];
+        if (row >= 0 && row < a.cap_src) vec[i] = ld_nc_v4(src + (int64_t)row * a.d + (id - r * vpr) * VE);
+      }
     }
   }
   // Magnitudes compare as their bits. Infinities and NaN, which do not count (infinities saturate, NaN stays NaN), show as
@@ -180,7 +184,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv8_select_kernel(const Kv8Evi
     double t[kFlight];
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) t[k] = 0.0;
-#pragma unroll 4
     for (int g = 0; g < heads; ++g) {        // summed in 64 bits, in head order
       float f[kFlight];
 #pragma unroll
@@ -231,8 +234,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv8_select_kernel(const Kv8Evi
     }
     if (lane == 31) wsum[w] = run;
     __syncthreads();
-    uint32_t above = run - (c0 + c1);
-    for (int i = 0; i < 32; ++i) above += i < w ? wsum[i] : 0u;
+    const uint32_t above = run - (c0 + c1) + __reduce_add_sync(0xffffffffu, lane < w ? wsum[lane] : 0u);
     if (above < need && need <= above + c0 + c1) {      // exactly one thread of the CTA
       const bool first = need <= above + c0;
       s_bin = (uint32_t)(kBins - 1 - 2 * tid) - (first ? 0u : 1u);
@@ -259,13 +261,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv8_select_kernel(const Kv8Evi
     wsum2[w] = eq;
   }
   __syncthreads();
-  uint32_t gt_before = 0, eq_before = 0, gt_all = 0, eq_all = 0;
-  for (int i = 0; i < 32; ++i) {
-    gt_before += i < w ? wsum[i] : 0u;
-    eq_before += i < w ? wsum2[i] : 0u;
-    gt_all += wsum[i];
-    eq_all += wsum2[i];
-  }
+  uint32_t gt_before = __reduce_add_sync(0xffffffffu, lane < w ? wsum[lane] : 0u);
+  uint32_t eq_before = __reduce_add_sync(0xffffffffu, lane < w ? wsum2[lane] : 0u);
+  const uint32_t gt_all = __reduce_add_sync(0xffffffffu, wsum[lane]), eq_all = __reduce_add_sync(0xffffffffu, wsum2[lane]);
   if (tid == 0) {
     counts[0] = gt_all;
     counts[1] = eq_all;
@@ -308,6 +306,7 @@ __global__ void __launch_bounds__(kThreads) kv8_gather_kernel(const Kv8EvictArgs
   constexpr int S = TG / 2, GROUPS = kThreads / TG;
   __shared__ int src_s[GROUPS][S];
   __shared__ float sc_s[GROUPS][2][S];
+  __shared__ float top_s[2][kThreads / 32];
   const int tid = threadIdx.x, gt = tid % TG, grp = tid / TG;
   const int64_t unit = (int64_t)blockIdx.x * GROUPS + grp;
   const bool live = unit < (int64_t)a.B * a.Hkv * runs;
@@ -318,23 +317,31 @@ __global__ void __launch_bounds__(kThreads) kv8_gather_kernel(const Kv8EvictArgs
   const int t0 = run * S, rows = live ? min(S, keep - t0) : 0;
   const int64_t sel = a.per_head ? bh : b;
   const int64_t runs_in = (a.cap + S - 1) / S, runs_out = (a.cap_out + S - 1) / S;
+  float sk = 0.f, sv = 0.f;
   if (gt < rows) {
     const int j = index[sel * a.n_keep + t0 + gt];
     src_s[grp][gt] = j;
-    sc_s[grp][0][gt] = a.k_scale[bh * runs_in + j / S];
-    sc_s[grp][1][gt] = a.v_scale[bh * runs_in + j / S];
+    sc_s[grp][0][gt] = sk = a.k_scale[bh * runs_in + j / S];
+    sc_s[grp][1][gt] = sv = a.v_scale[bh * runs_in + j / S];
     a.mass_out[bh * (int64_t)a.cap_out + t0 + gt] = a.mass[bh * (int64_t)a.cap + j];
+  }
+  sk = warp_max(sk);
+  sv = warp_max(sv);
+  if ((tid & 31) == 0) {
+    top_s[0][tid >> 5] = sk;
+    top_s[1][tid >> 5] = sv;
   }
   __syncthreads();
   if (rows <= 0) return;
   // S d / 16 vectors of K and as many of V, at most 4 of each per thread (d <= 128), all loaded before the first is used
   const int vpr = a.d / 16, nvec = rows * vpr;
+  const int per = (65536 + vpr - 1) / vpr;        // id / vpr = id * per >> 16 for id < 1024 and vpr <= 8
   uint4 vec[2][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int id = gt + i * TG;
     if (id < nvec) {
-      const int r = id / vpr;
+      const int r = id * per >> 16;
       const int64_t at = bh * (int64_t)a.cap * a.d + (int64_t)src_s[grp][r] * a.d + (id - r * vpr) * 16;
       vec[0][i] = ld_nc_v4(a.k_codes + at);
       vec[1][i] = ld_nc_v4(a.v_codes + at);
@@ -344,14 +351,14 @@ __global__ void __launch_bounds__(kThreads) kv8_gather_kernel(const Kv8EvictArgs
   for (int kv = 0; kv < 2; ++kv) {
     float top = 0.f;
 #pragma unroll
-    for (int r = 0; r < S; ++r) top = fmaxf(top, r < rows ? sc_s[grp][kv][r] : 0.f);
+    for (int i = 0; i < (S + 31) / 32; ++i) top = fmaxf(top, top_s[kv][grp * (TG / 32) + i]);
     uint8_t* dst = (kv ? a.v_out : a.k_out) + (bh * (int64_t)a.cap_out + t0) * a.d;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int id = gt + i * TG;
       if (id >= nvec) break;
       uint4 u = vec[kv][i];
-      const float old = sc_s[grp][kv][id / vpr];
+      const float old = sc_s[grp][kv][id * per >> 16];
       if (old != top) {
         const float ratio = top > 0.f ? old / top : 0.f;
         float f[16];
