@@ -49,7 +49,7 @@ constexpr int KT = 128;                    // keys per tile = rows per unit
 constexpr int KSTAGE = 128 * 128;          // K or V codes of a tile: 16 KB
 constexpr int VTILE = 2 * 128 * 64 * 2;    // V of a tile as f16: two 64-wide chunks of 16 KB
 constexpr int VCHUNK = VTILE / 2;
-constexpr int NK = 3, NV = 4, NB = 2;      // stages of the K and V code rings; f16 V buffers
+constexpr int NK = 3, NV = 2, NB = 2;      // stages of the K and V code rings; f16 V buffers
 constexpr float kMost = 30000.f;           // 32 weights that add up to more move the reference
 constexpr float kOff = 2.f;                // P is 2^2 times the weight relative to the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -84,6 +84,19 @@ DLLM_DEV bool wait_for(uint64_t* bar, uint32_t parity, int* abort_flag, int code
   return ok != 0;
 }
 
+// Whether the phase of the given parity is complete, without waiting.
+DLLM_DEV bool ready(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // n / d for 0 <= n < 2^31 (n * m >> shift; see attn_tc.cu).
 struct FastDiv {
   uint32_t m, shift;
@@ -96,7 +109,7 @@ FastDiv fast_div(int d) {
 }
 
 struct Bars {
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];          // Q of a unit, staged while the unit before is worked on
   uint64_t k_full[NK], k_empty[NK];
   uint64_t k_grant[NK];                    // a free K stage handed to the converters, for own rows
   uint64_t v_full[NV], v_empty[NV];
@@ -109,12 +122,12 @@ struct Bars {
   int abort_flag;
   int walk[7];                             // b, h, rt, first tile, number of tiles of this CTA, prefix length of b; all tiles
   uint32_t red[2][4];                      // own rows' largest magnitudes (bf16 bits), by converter warp
-  float qscale[KT];                        // per row: 2^k * scale * log2(e)
+  float qscale[2][KT];                     // per row: 2^k * scale * log2(e)
   float4 run[4][8];                        // per prefix tile and 16 keys: k scale, log2(v scale), 1 / v scale
   float4 run_own[NB];                      // of an own tile
   float2 ml[2][2][KT];                     // [unit parity][group][row]: reference and sum
 };
-constexpr int SMEM = 1024 + 2 * KSTAGE /*Q*/ + NK * KSTAGE + NV * KSTAGE + NB * VTILE + (int)sizeof(Bars);
+constexpr int SMEM = 1024 + 4 * KSTAGE /*Q*/ + NK * KSTAGE + NV * KSTAGE + NB * VTILE + (int)sizeof(Bars);
 static_assert(SMEM <= 232448, "shared memory budget");
 static_assert(SMEM > 233472 / 2, "tensor-memory kernels must not share an SM");
 
@@ -417,8 +430,8 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                    const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = base;                          // hi, lo
-  uint8_t* sK = sQ + 2 * KSTAGE;               // [NK]
+  uint8_t* sQ = base;                          // [2][hi, lo]
+  uint8_t* sK = sQ + 4 * KSTAGE;               // [NK]
   uint8_t* sW = sK + NK * KSTAGE;              // [NB] f16 V
   uint8_t* sV = sW + NB * VTILE;               // [NV]
   Bars& bar = *reinterpret_cast<Bars*>(sV + NV * KSTAGE);
@@ -427,8 +440,10 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 
   if (tid == 0) {
     bar.abort_flag = 0;
-    tc::mbar_init(&bar.q_full, 8);
-    tc::mbar_init(&bar.q_empty, 1 + 8);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bar.q_full[i], 8);
+      tc::mbar_init(&bar.q_empty[i], 1 + 8);
+    }
     for (int i = 0; i < NK; ++i) {
       tc::mbar_init(&bar.k_full[i], 1);
       tc::mbar_init(&bar.k_empty[i], 1);
@@ -537,10 +552,23 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       int j = 0, n = te - ts;                         // next tile and number of tiles of w's unit
       uint32_t k = 0, kph = 0, it_s = 0, seg_s = 0, it = 0, g = 0, ph = 0, seg = 0;
       int ahead = 0;
+      uint32_t idle = 0;
       bool q_ready = false;
       while (w.n > 0) {
-        if (ahead < 2 && ws.n > 0 && seg_s <= seg + 1) {
-          if (!q_ready && !wait_for(&bar.q_full, seg_s & 1, &bar.abort_flag, ST_TIMEOUT_MMA)) break;
+        const bool can_s = ahead < 2 && ws.n > 0 && seg_s <= seg + 1;
+        // an S whose operands are not there yet (a unit's own rows, the next unit's queries) does not hold up a P V
+        bool go = can_s;
+        if (can_s) {
+          const bool two = ts >= ws.tp && ws.own > 0;
+          if (ahead == 0) {
+            if (!q_ready && !wait_for(&bar.q_full[seg_s & 1], (seg_s >> 1) & 1, &bar.abort_flag, ST_TIMEOUT_MMA)) break;
+          } else {
+            go = (q_ready || ready(&bar.q_full[seg_s & 1], (seg_s >> 1) & 1)) && ready(&bar.k_full[k], kph) &&
+                 (!two || ready(&bar.k_full[k + 1 == NK ? 0 : k + 1], k + 1 == NK ? kph ^ 1 : kph));
+          }
+        }
+        if (go) {
+          idle = 0;
           q_ready = true;
           const bool own = ts >= ws.tp && ws.own > 0;
           const uint32_t d = tS + (it_s & 1) * 128;
@@ -550,10 +578,10 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             ok = ok && wait_for(&bar.k_full[k], kph, &bar.abort_flag, ST_TIMEOUT_MMA);
             if (!ok) break;
             tc::fence_after_sync();
-            const uint64_t dk = dK + k * (KSTAGE >> 4);
+            const uint64_t dk = dK + k * (KSTAGE >> 4), dq = dQ + (seg_s & 1) * (2 * KSTAGE >> 4);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)      // hi, then lo
-              mma_f8(d, dQ + (kk >> 2) * (KSTAGE >> 4) + (kk & 3) * 2, dk + (kk & 3) * 2, id_s, part != 0 || kk != 0);
+              mma_f8(d, dq + (kk >> 2) * (KSTAGE >> 4) + (kk & 3) * 2, dk + (kk & 3) * 2, id_s, part != 0 || kk != 0);
             tc::mma_commit(&bar.k_empty[k]);
             if (++k == NK) {
               k = 0;
@@ -565,7 +593,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           ++it_s;
           ++ahead;
           if (++ts == te) {
-            tc::mma_commit(&bar.q_empty);
+            tc::mma_commit(&bar.q_empty[seg_s & 1]);
             ws.next(p);
             ts = 0;
             te = ws.n > 0 ? ws.end() : 0;
@@ -573,6 +601,18 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             q_ready = false;
           }
           continue;
+        }
+        if (can_s) {      // neither may block the other: look again
+          if ((j == 0 && seg > 0 && !ready(&bar.o_free, (seg - 1) & 1)) || !ready(&bar.w_full[g], ph) ||
+              !ready(&bar.p_ready[it & 1], (it >> 1) & 1)) {
+            if (*abort_flag) break;
+            if (++idle > (1u << 24)) {
+              *abort_flag = ST_TIMEOUT_MMA;
+              break;
+            }
+            continue;
+          }
+          idle = 0;
         }
         if (j == 0 && seg > 0 && !wait_for(&bar.o_free, (seg - 1) & 1, &bar.abort_flag, ST_TIMEOUT_MMA)) break;
         if (!wait_for(&bar.w_full[g], ph, &bar.abort_flag, ST_TIMEOUT_MMA) ||
@@ -644,16 +684,24 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     uint32_t k = 0, v = 0, vph = 0, g = 0, wph = 1, seg = 0, granted = 0;
     for (; w.n > 0; w.next(p), ++seg) {
       const int64_t bh = (int64_t)w.b * a.Hkv + w.h;
-      if (seg > 0) {   // the first unit's Q is staged by the softmax warps, which have nothing to do yet
+      // the next unit's queries, staged when this unit's first tiles are on their way (the first unit's by the softmax
+      // warps, which have nothing to do yet)
+      const int t_end = w.end(), t_stage = min(w.ta + 2, t_end) - 1;
+      auto stage_next = [&]() {
+        Walk nx = w;
+        nx.next(p);
+        if (nx.n <= 0) return;
+        const uint32_t qb = (seg + 1) & 1;
         Quarter q;
-        load_q(p, w.b, w.h, w.rt, ct, q);      // before the wait for the previous unit's last S
-        wait_for(&bar.q_empty, (seg - 1) & 1, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
-        stage_q(p, w.b, w.h, w.rt, ct, 128, sQ, bar.qscale, q);
+        load_q(p, nx.b, nx.h, nx.rt, ct, q);
+        if (seg >= 1)
+          wait_for(&bar.q_empty[qb], (((seg + 1) >> 1) - 1) & 1, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
+        stage_q(p, nx.b, nx.h, nx.rt, ct, 128, sQ + qb * 2 * KSTAGE, bar.qscale[qb], q);
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_n(&bar.q_full, 2);
-      }
-      for (int t = w.ta; t < w.end(); ++t) {
+        if (lane == 0) arrive_n(&bar.q_full[qb], 2);
+      };
+      for (int t = w.ta; t < t_end; ++t) {
         uint8_t* dst = sW + g * VTILE;
         if (t < w.tp) {
           const int n = min(KT, w.len - t * KT);
@@ -755,6 +803,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           g = 0;
           wph ^= 1;
         }
+        if (t == t_stage) stage_next();
       }
     }
   } else {
@@ -769,18 +818,18 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     if (w.n > 0) {
       Quarter q;
       load_q(p, w.b, w.h, w.rt, tid - 128, q);
-      stage_q(p, w.b, w.h, w.rt, tid - 128, 256, sQ, bar.qscale, q);
+      stage_q(p, w.b, w.h, w.rt, tid - 128, 256, sQ, bar.qscale[0], q);
       fence_async_smem();
-      arrive(&bar.q_full);
+      arrive(&bar.q_full[0]);
     }
     for (; w.n > 0; w.next(p), ++seg) {
       const int R = w.rt * KT + row;
       const bool live = R < p.n_rows, warp_live = w.rt * KT + (warp & 3) * 32 < p.n_rows;
       const int qi = p.by_G(live ? R : p.n_rows - 1);
       const int own_lim = a.k_own ? visible_own(p, qi) : 0;
-      wait_for(&bar.q_full, seg & 1, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
-      const float rowc = bar.qscale[row];
-      arrive(&bar.q_empty);
+      wait_for(&bar.q_full[seg & 1], (seg >> 1) & 1, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
+      const float rowc = bar.qscale[seg & 1][row];
+      arrive(&bar.q_empty[seg & 1]);
       float mg = -INFINITY, l = 0.f;      // reference and sum of this group's tiles
       uint32_t lastg = 0, lastph = 0;     // V buffer and phase of the group's last tile
       bool any = false;                   // the group has had a tile of this unit
