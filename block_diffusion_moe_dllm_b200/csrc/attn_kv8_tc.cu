@@ -27,9 +27,13 @@
 // descriptor (measured on bare loops: 512 clocks per 8 MMAs of one kind, 756 when S and P V alternate, whatever their
 // operand sources), so about 1510 clocks, against 1420 for the tile's bytes at one SM's share of the HBM rate and 1024
 // for its exponentials. Two softmax groups of four warps take alternate tiles, one thread per row, each with an S and an O
-// of its own in TMEM and references of its own; their results are joined at the end of a unit. Measured on the way, 8
-// rows of 32768 keys, 512 query rows a kv head: two threads per row on the same tile 134 us; one O with a reference that
-// the groups pass on to each other and a pass for the maximum 105 us.
+// of its own in TMEM and references of its own; their results are joined at the end of a unit. Measured on the way, 8 x 32
+// queries of 16 heads over 32768 keys: two threads per row on the same tile 134 us; one O with a reference that the groups
+// pass on to each other and a pass for the maximum 105 us.
+// Measured (with the joining kernel): those 8 rows 95-110 us (2.4-2.9 TB/s of codes, 0.4 of the bf16 tensor rate), 16 x 32
+// queries over up to 2688 keys 33 us, one row over 1024 keys 14.5 us. Bound by a group's chain (its S waits for the P V
+// before it: about 2100 clocks a tile with two groups in flight), in small calls by set-up (2 us to the first load, 5 to
+// the first score) and the joining kernel.
 //
 // Roles: warp 0 TMA, warp 1 MMA, warps 2 and 3 the runs' scales (alternate prefix tiles), warps 4-7 and 8-11 softmax (even
 // and odd tiles), warps 12-15 convert Q, V and the own rows. Warps whose rows are all past the last only
