@@ -54,6 +54,10 @@ constexpr int KSTAGE = 128 * 128;          // K or V codes of a tile: 16 KB
 constexpr int VTILE = 2 * 128 * 64 * 2;    // V of a tile as f16: two 64-wide chunks of 16 KB
 constexpr int VCHUNK = VTILE / 2;
 constexpr int NK = 3, NV = 2, NB = 2;      // stages of the K and V code rings; f16 V buffers
+// Key tiles that a unit's end (products, merge of the halves, output, the next unit's start) counts for in the CTAs' shares.
+// Measured with 0 / 3 / 4 / 5 / 8 (us): 16 x 2688 33.0 / 30.2 / 30.0 / 30.9 / 31.9, 8 x 32768 95.7 / 92.0 / 91.6 / 91.7 /
+// 92.6, 64 x 4001 single tokens 83.0 / 73.9 / 71.7 / 71.7 / 74.8, 2 x 500 rows on 4000 keys 83.6 / 81.6 / 83.7 / 81.2 / 84.0.
+constexpr int kUnitEnd = 4;
 constexpr float kMost = 30000.f;           // 32 weights that add up to more move the reference
 constexpr float kOff = 2.f;                // P is 2^2 times the weight relative to the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -141,6 +145,7 @@ struct Params {
   FastDiv by_G, by_blk;
   int s_shift;                // log2 of scale_len
   int64_t own_sum;            // own key tiles of all row tiles of a (b, kv head)
+  int extra;                  // key tiles that a unit's end counts for in the shares (see Walk)
   int n_cta;
   float* part;                // [n_cta][2][kPart]
   int2* span;                 // [units]: first and last CTA that work on the unit (one alone has written its rows)
@@ -155,11 +160,12 @@ DLLM_DEV int own_keys(const Params& p, int rt) {
   return visible_own(p, p.by_G(min((rt + 1) * KT, p.n_rows) - 1));
 }
 DLLM_DEV int cdiv128(int x) { return (int)(((unsigned)x + 127u) >> 7); }
-// Key tiles of all units of batch row b: at least one per unit, so that rows without keys are written too. The host
-// checks that all of them stay below 2^31.
+// Key tiles of all units of batch row b, at least one per unit, so that rows without keys are written too, and each unit's
+// extra ones. The host checks that all of them stay below 2^31.
 DLLM_DEV uint32_t row_tiles(const Params& p, int b) {
   const int tp = cdiv128(kv8::prefix_len(p.a.lens, b, p.a.P));
-  return (uint32_t)p.a.Hkv * ((uint32_t)p.n_rt * (uint32_t)(p.a.k_own ? tp : max(tp, 1)) + (uint32_t)p.own_sum);
+  return (uint32_t)p.a.Hkv *
+         ((uint32_t)p.n_rt * (uint32_t)((p.a.k_own ? tp : max(tp, 1)) + p.extra) + (uint32_t)p.own_sum);
 }
 
 // CTA c's share of T tiles: the first T mod n CTAs take one more than the others.
@@ -173,10 +179,12 @@ struct Share {
   }
 };
 
-// Position in the sequence of key tiles, advanced unit by unit; every role walks it by itself.
+// Position in the sequence of key tiles, advanced unit by unit; every role walks it by itself. Behind its key tiles a unit
+// has p.extra that stand for the cost of its end and are no work themselves: a share that begins in them begins with the
+// next unit, so that CTAs which finish a unit get fewer tiles.
 struct Walk {
-  int b, h, rt, ta, n;      // unit, first tile in it, tiles left to this CTA
-  int len, tp, own, tiles;  // of the unit: prefix length, prefix tiles, own keys, all tiles
+  int b, h, rt, ta, n;      // unit, first tile in it, tiles left to this CTA (extra ones included)
+  int len, tp, own, tiles;  // of the unit: prefix length, prefix tiles, own keys, key tiles
   DLLM_DEV void unit(const Params& p) {
     own = own_keys(p, rt);
     tiles = max(1, tp + cdiv128(own));
@@ -184,11 +192,14 @@ struct Walk {
   DLLM_DEV void start(const Params& p, const int* w) {
     b = w[0]; h = w[1]; rt = w[2]; ta = w[3]; n = w[4]; len = w[5];
     tp = cdiv128(len);
-    if (n > 0) unit(p);
+    if (n > 0) {
+      unit(p);
+      if (ta >= tiles) next(p);
+    }
   }
-  DLLM_DEV int end() const { return min(tiles, ta + n); }    // the CTA's tiles of this unit: [ta, end())
+  DLLM_DEV int end() const { return min(tiles, ta + n); }    // the CTA's key tiles of this unit: [ta, end()), never empty
   DLLM_DEV void next(const Params& p) {
-    n -= end() - ta;
+    n -= min(tiles + p.extra - ta, n);
     ta = 0;
     if (++rt == p.n_rt) {
       rt = 0;
@@ -243,7 +254,7 @@ DLLM_DEV void make_walk(const Params& p, int* walk) {
     const int len = kv8::prefix_len(a.lens, b, a.P), tp = cdiv128(len);
     int rt = 0;
     for (; rt + 1 < p.n_rt; ++rt) {
-      const uint32_t t = (uint32_t)max(1, tp + cdiv128(own_keys(p, rt)));
+      const uint32_t t = (uint32_t)(max(1, tp + cdiv128(own_keys(p, rt))) + p.extra);
       if (rem < t) break;
       rem -= t;
     }
@@ -961,7 +972,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       if (tid == 128 && w.ta == 0) {
         const Share share((uint32_t)bar.walk[6], p.n_cta);
         const uint32_t first = share.first(blockIdx.x + 1) - (uint32_t)w.n;
-        const int last = (int)share.cta_of(first + (uint32_t)w.tiles - 1);
+        const int last = (int)share.cta_of(first + (uint32_t)w.tiles - 1);      // its last key tile's
         p.span[((int64_t)w.b * a.Hkv + w.h) * p.n_rt + w.rt] = make_int2((int)blockIdx.x, last);
       }
       arrive(&bar.o_free);
@@ -1354,9 +1365,12 @@ int launch_attn_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
   p.part = static_cast<float*>(a.ws);
   p.span = reinterpret_cast<int2*>(p.part + (size_t)num_sms() * 2 * kPart);
   p.reuse = p.n_rt > 1;
-  // most tiles there can be (lengths may be shorter): no more CTAs than those
+  // most tiles there can be (lengths may be shorter): no more CTAs than those. With a CTA for every tile the ends are not
+  // counted: the extra tiles would only bring CTAs without work (block of 1 x 1024: 14.3 us without them, 14.5 with)
   const int64_t tp = (a.P + KT - 1) / KT;
-  const int64_t most = (int64_t)a.B * a.Hkv * (p.n_rt * (a.k_own ? tp : std::max<int64_t>(tp, 1)) + p.own_sum);
+  int64_t most = (int64_t)a.B * a.Hkv * (p.n_rt * (a.k_own ? tp : std::max<int64_t>(tp, 1)) + p.own_sum);
+  p.extra = most > num_sms() ? kUnitEnd : 0;
+  most += (int64_t)a.B * a.Hkv * p.n_rt * p.extra;
   DLLM_REQUIRE(most < (1ll << 31), DLLM_ERR_UNSUPPORTED, "block_attn_kv8: too many rows and keys for one call");
   p.n_cta = (int)std::min<int64_t>(num_sms(), most);
   CUtensorMap mk, mv;
