@@ -300,6 +300,16 @@ def _device_stream(t, stream):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(current)
 
 
+def _stream_workspace(ws, need, device, stream):
+    """ws, or a new one, of at least `need` bytes. Memory taken here belongs to the call's stream: the fill comes before
+    the call, and whoever gets the memory next comes after it."""
+    if ws is not None and ws.nbytes >= need:
+        return ws
+    import torch
+    with torch.cuda.stream(stream):
+        return Workspace(need, device) if ws is None else ws.ensure(need)
+
+
 def kv8_store(k, v, k_codes, v_codes, k_scale, v_scale, B, Hkv, d, n, cap_src, cap, scale_len, dtype, src_row=0,
               dst_row=0, src_pos=None, dst_rows=None, pos_stride=None, stream=None):
     """Quantise n rows of K and V of every (row, kv head) into the 8-bit cache (E4M3 codes, a scale per run)."""
@@ -316,7 +326,7 @@ def block_attn_kv8(q, k_codes, v_codes, k_scale, v_scale, out, B, Lq, Hq, Hkv, d
     lib = load()
     desc = AttnKv8Desc(B, Lq, Hq, Hkv, d, blk_len, P, cap, cap_own, scale_len, dtype, scale)
     need = lib.dllm_block_attn_kv8_workspace_size(C.byref(desc))
-    ws = (ws or Workspace(need, q.device)).ensure(need)
+    ws = _stream_workspace(ws, need, q.device, stream)
     return check(lib.dllm_block_attn_kv8(C.byref(desc), ptr(q), ptr(k_codes), ptr(v_codes), ptr(k_scale),
                                          ptr(v_scale), ptr(prefix_len), ptr(k_own), ptr(v_own), ptr(out), ptr(lse),
                                          ws.addr, ws.nbytes, _device_stream(q, stream)))
@@ -328,7 +338,7 @@ def attn_mass_kv8(q, k_codes, k_scale, lse, mass_in, mass_out, B, Lq, Hq, Hkv, d
     lib = load()
     desc = AttnMassDesc(B, Lq, Hq, Hkv, d, P, cap, scale_len, dtype, scale, decay)
     need = lib.dllm_attn_mass_kv8_workspace_size(C.byref(desc))
-    ws = (ws or Workspace(need, q.device)).ensure(need)
+    ws = _stream_workspace(ws, need, q.device, stream)
     return check(lib.dllm_attn_mass_kv8(C.byref(desc), ptr(q), ptr(k_codes), ptr(k_scale), ptr(prefix_len), ptr(lse),
                                         ptr(mass_in), ptr(mass_out), ws.addr, ws.nbytes, _device_stream(q, stream)))
 
@@ -340,7 +350,7 @@ def kv8_evict(k_codes, v_codes, k_scale, v_scale, mass, k_out, v_out, k_scale_ou
     lib = load()
     desc = Kv8EvictDesc(B, Hkv, d, P, cap, n_keep, cap_out, scale_len, n_first, n_last, per_head)
     need = lib.dllm_kv8_evict_workspace_size(C.byref(desc))
-    ws = (ws or Workspace(need, mass.device)).ensure(need)
+    ws = _stream_workspace(ws, need, mass.device, stream)
     return check(lib.dllm_kv8_evict(C.byref(desc), ptr(k_codes), ptr(v_codes), ptr(k_scale), ptr(v_scale), ptr(mass),
                                     ptr(prefix_len), ptr(pos), ptr(k_out), ptr(v_out), ptr(k_scale_out),
                                     ptr(v_scale_out), ptr(mass_out), ptr(keep_pos), ptr(len_out), ws.addr, ws.nbytes,

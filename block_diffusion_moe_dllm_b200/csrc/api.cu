@@ -531,8 +531,30 @@ int check_kv8_format(const char* who, int d, int scale_len) {
   return DLLM_OK;
 }
 
-// What the two attention calls check alike; the largest launch grid is one CTA per 64 query rows of a (b, kv head), or
+// Rows and keys that one attention call takes: the largest launch grid is one CTA per 64 query rows of a (b, kv head), or
 // one per 32 keys.
+bool attn_kv8_fits(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t P) {
+  const int64_t rows = Lq * (Hq / Hkv), bh = B * Hkv;
+  return rows <= (1 << 24) && bh <= (1 << 24) && bh * (rows / 64 + 1) <= (1 << 24) && P <= (1 << 30) &&
+         bh * (P / 32 + 1) <= (1 << 30);
+}
+
+// No output (of the first n_out of a call's `count` arrays) shares memory with another array. Array i starts at p[i] and
+// has n[i] bytes.
+bool outputs_apart(const void* const* p, const size_t* n, int count, int n_out) {
+  for (int i = 0; i < n_out; ++i)
+    for (int j = i + 1; j < count; ++j)
+      if (overlaps(p[i], n[i], p[j], n[j])) return false;
+  return true;
+}
+
+// Bytes from the first to the last scale that a call on P rows of every (b, kv head) reads.
+size_t kv8_scales_read(size_t bh, int cap, int P, int scale_len) {
+  const size_t runs = ((size_t)cap + scale_len - 1) / scale_len;
+  return P ? ((bh - 1) * runs + ((size_t)P + scale_len - 1) / scale_len) * 4 : 0;
+}
+
+// What the two attention calls check alike.
 int check_attn_kv8(const char* who, int B, int Lq, int Hq, int Hkv, int d, int P, int cap, int scale_len, int dtype) {
   REQ(B >= 1 && Lq >= 1 && Hq >= 1 && Hkv >= 1 && P >= 0, DLLM_ERR_SHAPE, "%s: non-positive dimension", who);
   REQ(Hq % Hkv == 0, DLLM_ERR_SHAPE, "%s: Hq must be a multiple of Hkv", who);
@@ -541,9 +563,7 @@ int check_attn_kv8(const char* who, int B, int Lq, int Hq, int Hkv, int d, int P
   const int st = check_kv8_format(who, d, scale_len);
   if (st) return st;
   REQ(dtype == DLLM_F32 || d == 128, DLLM_ERR_UNSUPPORTED, "%s: bf16 needs head dim 128", who);
-  REQ((int64_t)Lq * (Hq / Hkv) <= (1 << 24) && (int64_t)B * Hkv * ((int64_t)Lq * (Hq / Hkv) / 64 + 1) <= (1 << 24) &&
-          (int64_t)B * Hkv * ((int64_t)P / 32 + 1) <= (1 << 30) && P <= (1 << 30),
-      DLLM_ERR_UNSUPPORTED, "%s: too many rows or keys for one call", who);
+  REQ(attn_kv8_fits(B, Lq, Hq, Hkv, P), DLLM_ERR_UNSUPPORTED, "%s: too many rows or keys for one call", who);
   return DLLM_OK;
 }
 
@@ -577,11 +597,9 @@ int dllm_kv8_store(const dllm_kv8_store_desc* d, const void* k, const void* v, c
   {
     const size_t bh = (size_t)d->B * d->Hkv, src = bh * d->cap_src * d->d * esize(d->dtype), cb = bh * d->cap * d->d,
                  sb = bh * ((d->cap + d->scale_len - 1) / d->scale_len) * 4;
-    const void* p[6] = {k, v, k_codes, v_codes, k_scale, v_scale};      // k and v may be the same
-    const size_t n[6] = {src, src, cb, cb, sb, sb};
-    for (int i = 0; i < 6; ++i)
-      for (int j = std::max(i + 1, 2); j < 6; ++j)
-        REQ(!overlaps(p[i], n[i], p[j], n[j]), DLLM_ERR_INVALID_ARG, "kv8_store: an output overlaps another array");
+    const void* const p[] = {k_codes, v_codes, k_scale, v_scale, k, v, dst_rows};      // k and v may be the same
+    const size_t n[] = {cb, cb, sb, sb, src, src, (size_t)d->B * 4};
+    REQ(outputs_apart(p, n, 7, 4), DLLM_ERR_INVALID_ARG, "kv8_store: an output overlaps another array");
   }
   if (d->n == 0) return DLLM_OK;
   Kv8StoreArgs a;
@@ -595,7 +613,9 @@ int dllm_kv8_store(const dllm_kv8_store_desc* d, const void* k, const void* v, c
 
 // Sizes are for both forms of the call, with and without own keys.
 size_t dllm_block_attn_kv8_workspace_size(const dllm_attn_kv8_desc* d) {
-  if (!d || d->B < 1 || d->Lq < 1 || d->Hkv < 1 || d->Hq < d->Hkv || d->P < 0) return 0;
+  if (!d || d->B < 1 || d->Lq < 1 || d->Hkv < 1 || d->Hq < d->Hkv || d->P < 0 || d->d < 1 || d->d > 128 ||
+      !attn_kv8_fits(d->B, d->Lq, d->Hq, d->Hkv, d->P))
+    return 0;
   return align256(kStatusBytes +
                   std::max(attn_kv8_workspace_bytes(d->B, d->Lq, d->Hq, d->Hkv, d->d, d->P, 1, d->dtype),
                            attn_kv8_workspace_bytes(d->B, d->Lq, d->Hq, d->Hkv, d->d, d->P, 0, d->dtype)));
@@ -615,8 +635,15 @@ int dllm_block_attn_kv8(const dllm_attn_kv8_desc* d, const void* q, const void* 
   REQ(aligned16(q) && aligned16(out) && aligned16(k_codes) && aligned16(v_codes) && aligned16(k_own) &&
           aligned16(v_own),
       DLLM_ERR_ALIGN, "block_attn_kv8: q, out, codes and own rows must be 16-byte aligned");
-  const size_t qb = (size_t)d->B * d->Lq * d->Hq * d->d * esize(d->dtype);
-  REQ(!overlaps(q, qb, out, qb), DLLM_ERR_INVALID_ARG, "block_attn_kv8: out overlaps q");
+  {
+    const size_t rows = (size_t)d->B * d->Lq * d->Hq, bh = (size_t)d->B * d->Hkv, qb = rows * d->d * esize(d->dtype);
+    // from the first to the last row that is read: a cache may be a part of a longer one
+    const size_t cb = d->P ? ((bh - 1) * d->cap + d->P) * d->d : 0, sb = kv8_scales_read(bh, d->cap, d->P, d->scale_len),
+                 ob = ((bh - 1) * d->cap_own + d->Lq) * d->d * esize(d->dtype);
+    const void* const p[] = {out, lse, q, k_codes, v_codes, k_scale, v_scale, k_own, v_own, prefix_len};
+    const size_t n[] = {qb, rows * 4, qb, cb, cb, sb, sb, ob, ob, (size_t)d->B * 4};
+    REQ(outputs_apart(p, n, 10, 2), DLLM_ERR_INVALID_ARG, "block_attn_kv8: an output overlaps another array");
+  }
   st = check_ws(ws, ws_bytes, dllm_block_attn_kv8_workspace_size(d));
   if (st) return st;
   Carver c(ws);
@@ -640,9 +667,14 @@ int dllm_attn_mass_kv8(const dllm_attn_mass_desc* d, const void* q, const void* 
   if (st) return st;
   REQ(d->P == 0 || (k_codes && k_scale), DLLM_ERR_INVALID_ARG, "attn_mass_kv8: NULL cache");
   REQ(aligned16(q) && aligned16(k_codes), DLLM_ERR_ALIGN, "attn_mass_kv8: q and codes must be 16-byte aligned");
-  const size_t mb = (size_t)d->B * d->Hkv * d->cap * 4;
-  REQ(mass_in == mass_out || !overlaps(mass_in, mb, mass_out, mb), DLLM_ERR_INVALID_ARG,
-      "attn_mass_kv8: mass_in and mass_out overlap in part");
+  {
+    const size_t rows = (size_t)d->B * d->Lq * d->Hq, bh = (size_t)d->B * d->Hkv, mb = bh * d->cap * 4;
+    const size_t cb = d->P ? ((bh - 1) * d->cap + d->P) * d->d : 0, sb = kv8_scales_read(bh, d->cap, d->P, d->scale_len);
+    const void* const p[] = {mass_out, mass_in == mass_out ? nullptr : mass_in, q, k_codes, k_scale, lse, prefix_len};
+    const size_t n[] = {mb, mb, rows * d->d * esize(d->dtype), cb, sb, rows * 4, (size_t)d->B * 4};
+    REQ(outputs_apart(p, n, 7, 1), DLLM_ERR_INVALID_ARG,
+        "attn_mass_kv8: mass_out overlaps another array (mass_in may be the same one)");
+  }
   st = check_ws(ws, ws_bytes, dllm_attn_mass_kv8_workspace_size(d));
   if (st) return st;
   if (d->P == 0) return DLLM_OK;
@@ -682,14 +714,12 @@ int dllm_kv8_evict(const dllm_kv8_evict_desc* d, const void* k_codes, const void
     const size_t sb = bh * ((d->cap + d->scale_len - 1) / d->scale_len) * 4,
                  so = bh * ((d->cap_out + d->scale_len - 1) / d->scale_len) * 4;
     const size_t hs = (size_t)d->B * (d->per_head ? d->Hkv : 1);
-    const void* in[7] = {k_codes, v_codes, k_scale, v_scale, mass, pos, prefix_len};
-    const size_t nin[7] = {cb, cb, sb, sb, bh * d->cap * 4, hs * d->cap * 4, (size_t)d->B * 4};
-    const void* out[7] = {k_out, v_out, k_scale_out, v_scale_out, mass_out, keep_pos, len_out};
-    const size_t nout[7] = {co, co, so, so, bh * d->cap_out * 4, hs * d->cap_out * 4, (size_t)d->B * 4};
-    for (int i = 0; i < 7; ++i)
-      for (int j = 0; j < 7; ++j)
-        REQ(!overlaps(in[i], nin[i], out[j], nout[j]) && (j <= i || !overlaps(out[i], nout[i], out[j], nout[j])),
-            DLLM_ERR_INVALID_ARG, "kv8_evict: an output overlaps another array");
+    const void* const p[] = {k_out,   v_out,   k_scale_out, v_scale_out, mass_out, keep_pos, len_out,
+                             k_codes, v_codes, k_scale,     v_scale,     mass,     pos,      prefix_len};
+    const size_t nb = (size_t)d->B * 4;
+    const size_t n[] = {co, co, so, so, bh * d->cap_out * 4, hs * d->cap_out * 4, nb,
+                        cb, cb, sb, sb, bh * d->cap * 4,     hs * d->cap * 4,     nb};
+    REQ(outputs_apart(p, n, 14, 7), DLLM_ERR_INVALID_ARG, "kv8_evict: an output overlaps another array");
   }
   st = check_ws(ws, ws_bytes, dllm_kv8_evict_workspace_size(d));
   if (st) return st;

@@ -3,8 +3,8 @@
 //
 // Work: the (query, head of the group) rows of a (batch row, kv head) are cut into tiles of 128 rows, each a unit of
 // ceil(len[b] / 128) prefix key tiles and the own key tiles its last query sees. All units' key tiles in a row are
-// dealt to one CTA per SM in equal contiguous shares, so rows of different lengths, few rows and many rows all keep
-// every SM on the same number of tiles; a unit that spans several CTAs leaves its partial results (unnormalised o, m, l
+// dealt to one CTA per SM in equal contiguous shares, a unit's end counting for some tiles too, so rows of different
+// lengths, few rows and many rows all keep every SM busy equally long; a unit that spans several CTAs leaves its partial results (unnormalised o, m, l
 // per row) in the workspace and a second kernel joins them.
 //
 // Per key tile of 128:
@@ -30,8 +30,8 @@
 // of its own in TMEM and references of its own; their results are joined at the end of a unit. Measured on the way, 8 x 32
 // queries of 16 heads over 32768 keys: two threads per row on the same tile 134 us; one O with a reference that the groups
 // pass on to each other and a pass for the maximum 105 us.
-// Measured (with the joining kernel): those 8 rows 95-110 us (2.4-2.9 TB/s of codes, 0.4 of the bf16 tensor rate), 16 x 32
-// queries over up to 2688 keys 33 us, one row over 1024 keys 14.5 us. Bound by a group's chain (its S waits for the P V
+// Measured (with the joining kernel): those 8 rows 92-103 us (2.6-2.9 TB/s of codes, 0.4 of the bf16 tensor rate), 16 x 32
+// queries over up to 2688 keys 30 us, one row over 1024 keys 14.5 us. Bound by a group's chain (its S waits for the P V
 // before it: about 2100 clocks a tile with two groups in flight), in small calls by set-up (2 us to the first load, 5 to
 // the first score) and the joining kernel.
 //

@@ -482,7 +482,7 @@ DLLM_API int dllm_kv8_store(const dllm_kv8_store_desc* desc, const void* k, cons
  *   k_own, v_own [B, Hkv, cap_own, d] in the storage type, rows [0, Lq) (both NULL: the prefix only)
  *   out          [B, Lq, Hq * d], 16-byte aligned; zeros where a query sees no key
  *   lse          [B, Lq, Hq] fp32 (nullable): log of the sum of exp(score) over the query's keys, -inf without keys
- * scale <= 0 selects 1/sqrt(d). Any Hq a multiple of Hkv. bf16: d == 128. Own V rows must be finite (a query's weight
+ * out and lse overlap no other array. scale <= 0 selects 1/sqrt(d). Any Hq a multiple of Hkv. bf16: d == 128. Own V rows must be finite (a query's weight
  * on a row it does not see is 0, and 0 times infinity is not). bf16 reads V scales below 2^-64 as 2^-64 and holds the
  * weights in f16 (11 bits; those below 2^-27 of the row's largest so far count as 0), their sums in fp32.
  */
@@ -507,8 +507,8 @@ DLLM_API size_t dllm_block_attn_kv8_workspace_size(const dllm_attn_kv8_desc* des
  *                       exp(score(i, g, j) - lse[b, i, g]),   j < prefix_len[b]
  * with the lse that dllm_block_attn_kv8 wrote for the same queries (rows of lse -inf add nothing). Sums in a fixed
  * order: the same inputs give the same bits.
- *   mass_in (nullable: zeros), mass_out [B, Hkv, cap] fp32, the same array or disjoint ones; rows past a prefix are
- *   left as they were.
+ *   mass_in (nullable: zeros), mass_out [B, Hkv, cap] fp32, the same array or disjoint ones, and no other array's memory;
+ *   rows past a prefix are left as they were.
  */
 typedef struct {
   int32_t B, Lq, Hq, Hkv, d;

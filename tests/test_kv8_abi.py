@@ -116,6 +116,71 @@ def test_workspace_sizes_of_refused_shapes_are_zero_or_plain(lib):
     assert lib.dllm_kv8_evict_workspace_size(C.byref(f)) > lib.dllm_kv8_evict_workspace_size(C.byref(e)) > 0
 
 
+@pytest.mark.parametrize("at", ["out=k_own", "out=v_own", "out=codes", "out=k_scale", "out=lens", "lse=out", "lse=q",
+                                "lse=v_scale"])
+def test_block_attn_kv8_refuses_outputs_on_other_arrays(lib, at):
+    p = dict(q=1 << 30, codes=2 << 30, vc=3 << 30, k_scale=4 << 30, v_scale=5 << 30, lens=6 << 30, k_own=7 << 30,
+             v_own=8 << 30, out=9 << 30, lse=10 << 30)
+    which, on = at.split("=")
+    d = bd.AttnKv8Desc(2, 32, 16, 4, 128, 32, 256, 256, 32, 32, bd.BF16, 0.0)
+
+    def call(ws):
+        return lib.dllm_block_attn_kv8(C.byref(d), *p.values(), ws, BIG, None)
+
+    assert call(None) == bd.ERR_WORKSPACE                    # these arrays are fine
+    # the last 16 bytes that the call reads of the other array (one row tensor each of 2 batch rows)
+    span = dict(q=2 * 32 * 16 * 128 * 2, codes=2 * 4 * 256 * 128, k_scale=2 * 4 * 8 * 4, v_scale=2 * 4 * 8 * 4, lens=8,
+                k_own=2 * 4 * 32 * 128 * 2, v_own=2 * 4 * 32 * 128 * 2, out=2 * 32 * 16 * 128 * 2)[on]
+    first = p[on]
+    p[which] = first + (span - 1) // 16 * 16
+    assert call(None) == bd.ERR_INVALID_ARG
+    p[which] = first + (span + 15) // 16 * 16
+    assert call(None) == bd.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("on,span", [(1, 2 * 32 * 16 * 128 * 2), (2, 2 * 4 * 256 * 128), (3, 2 * 4 * 8 * 4), (4, 8),
+                                     (5, 2 * 32 * 16 * 4)])
+def test_attn_mass_kv8_refuses_its_output_on_other_arrays(lib, on, span):
+    d = bd.AttnMassDesc(2, 32, 16, 4, 128, 256, 256, 32, bd.BF16, 0.0, 1.0)
+    p = [i << 30 for i in range(1, 6)]                       # q, codes, k_scale, lengths, lse
+    for off, code in ((span - 4, bd.ERR_INVALID_ARG), (span, bd.ERR_WORKSPACE)):
+        m = (on << 30) + off
+        assert lib.dllm_attn_mass_kv8(C.byref(d), *p, m, m, None, BIG, None) == code
+
+
+def test_store_refuses_an_output_on_its_row_list(lib):
+    assert _store(lib, dst_rows=(1 << 41) + 64) == bd.ERR_INVALID_ARG
+
+
+def test_workspace_size_of_more_rows_than_a_call_takes_is_zero(lib):
+    # rows per kv head of 2^32 and beyond, at which a 32-bit product is zero or negative
+    for Lq, Hq, B, P in ((1 << 16, 1 << 16, 1, 256), (1 << 17, 1 << 14, 1, 256), (32, 16, 1 << 30, 256), (1, 1, 1 << 24, 1 << 30)):
+        for dt in (bd.BF16, bd.F32):
+            d = bd.AttnKv8Desc(B, Lq, Hq, 1, 128, 32, P, P, 32, 32, dt, 0.0)
+            assert lib.dllm_block_attn_kv8_workspace_size(C.byref(d)) == 0
+
+
+def test_a_workspace_is_taken_on_the_calls_stream(monkeypatch):
+    """A workspace that a call takes or grows is filled on the call's stream, which also orders who gets it next."""
+    seen = []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            seen.append(self.stream)
+
+        def __exit__(self, *_):
+            seen.append("left")
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    ws = bd._stream_workspace(None, 1000, "cpu", "side")
+    assert seen == ["side", "left"] and ws.nbytes == 1000
+    assert bd._stream_workspace(ws, 1000, "cpu", "side") is ws and len(seen) == 2
+    assert bd._stream_workspace(ws, 5000, "cpu", "other").nbytes == 5000 and seen[2:] == ["other", "left"]
+
+
 # ------------------------------------------------------------------------------------------------ oracle pins
 def test_e4m3_values_and_rounding_match_torch():
     want = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
