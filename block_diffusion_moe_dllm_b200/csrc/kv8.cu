@@ -146,22 +146,6 @@ constexpr int kSelThreads = 1024, kBins = 2048;
 constexpr int kSelPart = 4096;              // positions for which a selection gets another CTA
 constexpr int kSelSmemKeys = 32768;         // keys of a part that fit shared memory
 
-DLLM_DEV void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-DLLM_DEV uint32_t peer_u32(const void* mine, uint32_t rank) {    // the same shared variable of another CTA of the cluster
-  uint32_t v, at;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
-
-DLLM_DEV void peer_store_u32(void* mine, uint32_t rank, uint32_t v) {
-  uint32_t at;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
-}
-
 __global__ void __launch_bounds__(kSelThreads, 1) kv8_select_kernel(const Kv8EvictArgs a, int C, uint32_t* __restrict__ keys,
                                                                     int32_t* __restrict__ index) {
   pdl_enter();
@@ -216,16 +200,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv8_select_kernel(const Kv8Evi
       const uint32_t u = key[i];
       if ((u & mask) == prefix) atomicAdd(&hs[(u >> shift) & ((1u << bits) - 1u)], 1u);
     }
-    cluster_sync();
+    kv8::cluster_sync();
     if (C > 1) {      // each CTA adds up its share of the bins over the cluster and gives every CTA the sums
       const int per = kBins / C;
       for (int i = tid; i < per; i += kSelThreads) {
         const int bin = rank * per + i;
         uint32_t t = 0;
-        for (int r = 0; r < C; ++r) t += peer_u32(&hs[bin], r);
-        for (int r = 0; r < C; ++r) peer_store_u32(&sums[bin], r, t);
+        for (int r = 0; r < C; ++r) t += kv8::peer_u32(&hs[bin], r);
+        for (int r = 0; r < C; ++r) kv8::peer_store_u32(&sums[bin], r, t);
       }
-      cluster_sync();
+      kv8::cluster_sync();
     }
     // thread t holds bins 2047 - 2 t and 2046 - 2 t: a prefix sum over the threads counts from the largest key down
     const uint32_t* tot = C > 1 ? sums : hs;
@@ -272,12 +256,12 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv8_select_kernel(const Kv8Evi
     counts[0] = gt_all;
     counts[1] = eq_all;
   }
-  cluster_sync();
+  kv8::cluster_sync();
   for (int r = 0; r < rank; ++r) {
-    gt_before += peer_u32(&counts[0], r);
-    eq_before += peer_u32(&counts[1], r);
+    gt_before += kv8::peer_u32(&counts[0], r);
+    eq_before += kv8::peer_u32(&counts[1], r);
   }
-  cluster_sync();        // no CTA leaves while another reads its counts
+  kv8::cluster_sync();        // no CTA leaves while another reads its counts
   const int32_t* pos = a.pos ? a.pos + (int64_t)sel * a.cap + lo : nullptr;
   int32_t* out = a.keep_pos + (int64_t)sel * a.cap_out;
   int32_t* idx = index + (int64_t)sel * a.n_keep;

@@ -55,5 +55,21 @@ DLLM_DEV float exp2i(int k) { return __uint_as_float((uint32_t)(k + 127) << 23);
 // Length of batch row b's prefix: the device lengths clamped to [0, P], or P without them.
 DLLM_DEV int prefix_len(const int32_t* lens, int b, int P) { return lens ? min(max(lens[b], 0), P) : P; }
 
+// Thread-block clusters: a barrier over all CTAs, and the same shared variable of another CTA.
+DLLM_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+DLLM_DEV uint32_t peer_u32(const void* mine, uint32_t rank) {
+  uint32_t v, at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+DLLM_DEV void peer_store_u32(void* mine, uint32_t rank, uint32_t v) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
 }  // namespace kv8
 }  // namespace dllm

@@ -297,6 +297,14 @@ def test_attn_mass_kv8(dtype, B, Lq, Hq, Hkv, d, P, S, lens, start):
     assert np.all(err <= bound), f"worst {np.max(err / bound):.3g} bounds"
 
 
+# few keys and several row tiles of 64: 8, 5, 3 and 2 of them shared by clusters of 8, 4, 2 and 2 CTAs (sums of at most 4
+# rows a tile, 16 threads and 8 CTAs: below 2^-19 of rounding, as in the bound above)
+@pytest.mark.parametrize("B,Lq,Hq,Hkv,d,P,S,lens", [(1, 32, 16, 1, 64, 70, 16, None), (3, 20, 32, 2, 128, 99, 32, (99, 0, 33)),
+                                                    (1, 65, 2, 1, 80, 40, 64, None), (2, 32, 20, 5, 32, 31, 16, (31, 1))])
+def test_attn_mass_kv8_f32_row_tiles(B, Lq, Hq, Hkv, d, P, S, lens):
+    test_attn_mass_kv8("f32", B, Lq, Hq, Hkv, d, P, S, lens, "same")
+
+
 # ------------------------------------------------------------------------------------------------ eviction
 EVICT = [(1, 1, 128, 1, 16, 1, 0, 0, None), (2, 4, 128, 300, 32, 150, 4, 64, (300, 171)),
          (3, 2, 64, 257, 16, 100, 0, 0, (257, 0, 99)), (2, 3, 128, 1500, 64, 1400, 1, 1, (1500, 1401)),
