@@ -147,6 +147,7 @@ struct Params {
   int64_t own_sum;            // own key tiles of all row tiles of a (b, kv head)
   int extra;                  // key tiles that a unit's end counts for in the shares (see Walk)
   int n_cta;
+  int merge_shift;            // log2 of the rows that a block of the joining kernel takes, 3 to 7
   float* part;                // [n_cta][2][kPart]
   int2* span;                 // [units]: first and last CTA that work on the unit (one alone has written its rows)
   int reuse;                  // several row tiles read the same keys: keep them in L2
@@ -986,14 +987,18 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   }
 }
 
-// Joins the partial results of the units that span several CTAs: one block per unit and 8 output columns, one thread
-// per row, the CTAs in order. Bound by the latency of its loads.
+// Joins the partial results of the units that span several CTAs, the CTAs in order: a thread takes 8 output columns of a
+// row. A block is as many rows as a unit has, rounded up to a power of two, and the column groups that fill it up to 128
+// threads: a full row tile takes 16 blocks, a single token's few heads one (see the launch). Bound by the latency of its
+// loads.
 constexpr int kMergeCols = 8;
+static_assert(KT * kMergeCols == 128 << 3, "16 column groups of 8: blocks per unit are rows / 8");
 __global__ void __launch_bounds__(KT) attn_kv8_merge_kernel(const __grid_constant__ Params p) {
   pdl_enter();
   const Kv8AttnArgs& a = p.a;
-  const int row = threadIdx.x, part_col = blockIdx.x % (128 / kMergeCols);
-  const int64_t unit = blockIdx.x / (128 / kMergeCols);
+  const int sh = p.merge_shift, row = threadIdx.x & ((1 << sh) - 1);
+  const int part_col = (int)((blockIdx.x & ((1u << (sh - 3)) - 1u)) << (7 - sh)) + (int)(threadIdx.x >> sh);
+  const int64_t unit = blockIdx.x >> (sh - 3);
   const int2 sp = p.span[unit];
   const int rt = (int)(unit % p.n_rt), R = rt * KT + row, n = sp.y - sp.x + 1;
   if (n == 1 || R >= p.n_rows) return;
@@ -1365,6 +1370,8 @@ int launch_attn_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
   p.part = static_cast<float*>(a.ws);
   p.span = reinterpret_cast<int2*>(p.part + (size_t)num_sms() * 2 * kPart);
   p.reuse = p.n_rt > 1;
+  p.merge_shift = 3;
+  while (p.merge_shift < 7 && (1 << p.merge_shift) < p.n_rows) ++p.merge_shift;
   // most tiles there can be (lengths may be shorter): no more CTAs than those. With a CTA for every tile the ends are not
   // counted: the extra tiles would only bring CTAs without work (block of 1 x 1024: 14.3 us without them, 14.5 with)
   const int64_t tp = (a.P + KT - 1) / KT;
@@ -1384,7 +1391,7 @@ int launch_attn_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
   launch_pdl(attn_kv8_tc_kernel, p.n_cta, NT, SMEM, s, mk, mv, p);
   DLLM_CHECK_LAUNCH("attn_kv8_tc_kernel");
   if (p.n_cta > 1) {
-    launch_pdl(attn_kv8_merge_kernel, (unsigned)((int64_t)a.B * a.Hkv * p.n_rt * (128 / kMergeCols)), KT, 0, s, p);
+    launch_pdl(attn_kv8_merge_kernel, (unsigned)(((int64_t)a.B * a.Hkv * p.n_rt) << (p.merge_shift - 3)), KT, 0, s, p);
     DLLM_CHECK_LAUNCH("attn_kv8_merge_kernel");
   }
   return DLLM_OK;
