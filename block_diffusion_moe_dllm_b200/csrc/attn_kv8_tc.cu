@@ -12,8 +12,9 @@
 //               to 2^-17.8 of their row's largest magnitude as two E4M3 parts: q * 2^-k brought to at most 448, hi =
 //               E4M3(q), lo = E4M3(q - hi) (bf16 has 8 significant bits, two parts of 4); both parts accumulate into the
 //               same fp32 S. fp8 MMAs run at twice the bf16 rate, so the two cost what one bf16 product would.
-//               Own keys are split the same way by the converter warps (two parts with one power-of-two scale per tile:
-//               four products).
+//               Own keys are split the same way by the converter warps (two parts: four products), each with a
+//               power-of-two scale of its own, and own V rows too: no row's precision depends on another row, least of all
+//               on one that the query does not see.
 //   softmax     one thread per row; x = S * (2^k scale log2(e) k_scale) + log2(v_scale) - m: the V scale of each run rides
 //               in the exponent, so that P V needs no scaled copy of V; the row sum divides it out again run by run.
 //               P = 2^(x + 2) as f16. The reference m is not a running maximum: it is the largest of the first 32 scores
@@ -44,6 +45,7 @@
 #include "kv8.h"
 #include "misc.h"
 #include <algorithm>
+#include <type_traits>
 
 namespace dllm {
 namespace {
@@ -116,6 +118,11 @@ FastDiv fast_div(int d) {
   return {(uint32_t)((((uint64_t)1 << (31 + sh)) + (uint64_t)d - 1) / (uint64_t)d), 31 + sh};
 }
 
+// Per key of an own tile: K scale, log2(V scale), 1 / V scale (read as pairs).
+struct OwnScales {
+  alignas(16) float k[KT], lv[KT], iv[KT];
+};
+
 struct Bars {
   uint64_t q_full[2], q_empty[2];          // Q of a unit, staged while the unit before is worked on
   uint64_t k_full[NK], k_empty[NK];
@@ -129,10 +136,10 @@ struct Bars {
   uint32_t tmem_base;
   int abort_flag;
   int walk[7];                             // b, h, rt, first tile, number of tiles of this CTA, prefix length of b; all tiles
-  uint32_t red[2][4];                      // own rows' largest magnitudes (bf16 bits), by converter warp
   float qscale[2][KT];                     // per row: 2^k * scale * log2(e)
   float4 run[4][8];                        // per prefix tile and 16 keys: k scale, log2(v scale), 1 / v scale
-  float4 run_own[NB];                      // of an own tile
+  float4 run_one;                          // a run whose scores are exponents already: 1, 0, 1
+  OwnScales own[NB];                       // of an own tile
   float2 ml[2][2][KT];                     // [unit parity][group][row]: reference and sum
 };
 constexpr int SMEM = 1024 + 4 * KSTAGE /*Q*/ + NK * KSTAGE + NV * KSTAGE + NB * VTILE + (int)sizeof(Bars);
@@ -364,9 +371,8 @@ DLLM_DEV float run_factor(float rowc, const float4& rs) {
   const float c = rowc * rs.x;
   return c < 1e-30f ? 1e-30f : c;
 }
-// 32 columns of S in one row, the first lim of them visible if partly.
-DLLM_DEV void load_scores(uint32_t at, bool partly, int lim, float* v) {
-  tmem_ld32(at, v);
+// The first lim of 32 columns are visible, if not all are.
+DLLM_DEV void mask_scores(bool partly, int lim, float* v) {
   if (partly) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = i < lim ? v[i] : -INFINITY;
@@ -384,6 +390,37 @@ DLLM_DEV float scores_max(const float* v, float rowc, const float4* run, int rst
     mt = fmaxf(mt, fmaf(m, run_factor(rowc, rs), rs.y));
   }
   return mt;
+}
+// 32 own keys' scores as exponents, x = S c + log2(V scale) with a factor c of each key. Before the mask, so c may be 0.
+DLLM_DEV void own_exponents(float* v, float rowc, const float* k, const float* lv) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 ks = *reinterpret_cast<const float4*>(k + i), ls = *reinterpret_cast<const float4*>(lv + i);
+    v[i] = fmaf(v[i], rowc * ks.x, ls.x);
+    v[i + 1] = fmaf(v[i + 1], rowc * ks.y, ls.y);
+    v[i + 2] = fmaf(v[i + 2], rowc * ks.z, ls.z);
+    v[i + 3] = fmaf(v[i + 3], rowc * ks.w, ls.w);
+  }
+}
+// The weights of 32 own keys' exponents as f16 pairs, their sum, and their sum with the keys' V scales divided out (l).
+DLLM_DEV float own_exp(const float* v, const float* iv, float shift, uint32_t* pk, float& l) {
+  const uint64_t d2 = pk2(shift, shift);
+  uint64_t s2 = pk2(0.f, 0.f), l2 = s2;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float x0, x1;
+    upk2(add2(pk2(v[2 * i], v[2 * i + 1]), d2), x0, x1);
+    const float e0 = ex2(x0), e1 = ex2(x1);
+    const uint64_t e2 = pk2(e0, e1);
+    pk[i] = f16x2(e0, e1);
+    s2 = add2(s2, e2);
+    l2 = fma2(e2, *reinterpret_cast<const uint64_t*>(iv + 2 * i), l2);
+  }
+  float s0, s1, l0, l1;
+  upk2(s2, s0, s1);
+  upk2(l2, l0, l1);
+  l = l0 + l1;
+  return s0 + s1;
 }
 // The weights of 32 columns as f16 pairs, their sum, and their sum with the V scales divided out (l).
 DLLM_DEV float scores_exp(const float* v, float rowc, const float4* run, int rstep, float shift, uint32_t* pk, float& l) {
@@ -456,6 +493,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 
   if (tid == 0) {
     bar.abort_flag = 0;
+    bar.run_one = make_float4(1.f, 0.f, 1.f, 0.f);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bar.q_full[i], 8);
       tc::mbar_init(&bar.q_empty[i], 1 + 8);
@@ -751,49 +789,41 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           }
           k = k == NK - 1 ? 0 : k + 1;
         } else {
-          // own rows (none at all in a unit without keys): four threads per key, 32 keys at a time
+          // own rows (none at all in a unit without keys): four threads per key, 32 keys at a time, the next 32 on their
+          // way (the first ones ahead of the waits)
           const int j0 = (t - w.tp) * KT, n = min(KT, w.own - j0), parts = n > 0 ? 2 : 1;
           const int64_t at = (bh * a.cap_own + j0) * 128 + 32 * (ct & 3);
-          // largest finite magnitudes (a row with an infinity or NaN counts as 0: K makes all its codes NaN)
-          uint32_t mk = 0, mv = 0;
-          auto load_own = [&](int r, Quarter& k8, Quarter& v8) {
+          Quarter k8, v8;
+          auto load_own = [&](int r) {
             k8.load(r < n ? static_cast<const __nv_bfloat16*>(a.k_own) + at + r * 128 : nullptr);
             v8.load(r < n ? static_cast<const __nv_bfloat16*>(a.v_own) + at + r * 128 : nullptr);
           };
-#pragma unroll 2
-          for (int r = ct >> 2; r - (ct >> 2) < n; r += 32) {
-            Quarter k8, v8;
-            load_own(r, k8, v8);
-            const uint32_t x = k8.amax(), y = v8.amax();
-            mk = max(mk, x < kInfBits ? x : 0u);
-            mv = max(mv, y < kInfBits ? y : 0u);
-          }
-          mk = __reduce_max_sync(0xffffffffu, mk);
-          mv = __reduce_max_sync(0xffffffffu, mv);
-          if (lane == 0) {
-            bar.red[0][cw] = mk;
-            bar.red[1][cw] = mv;
-          }
-          tc::named_bar_sync(kBarConv, 128);
-          const int ek = bits_exp(max(max(bar.red[0][0], bar.red[0][1]), max(bar.red[0][2], bar.red[0][3])));
-          const int ev = bits_exp(max(max(bar.red[1][0], bar.red[1][1]), max(bar.red[1][2], bar.red[1][3])));
+          load_own(ct >> 2);
           wait_for(&bar.w_empty[g], wph, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
-          if (ct == 0) bar.run_own[g] = make_float4(kv8::exp2i(ek), (float)ev, kv8::exp2i(-ev), 0.f);
           const uint32_t k0 = k, k1 = parts == 2 ? (k + 1) % NK : k;
           for (int i = 0; i < parts; ++i) {
             const uint32_t kk = i ? k1 : k0;
             wait_for(&bar.k_grant[kk], (granted >> kk) & 1, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
             granted ^= 1u << kk;
           }
-          const float ik = kv8::exp2i(-ek), iv = kv8::exp2i(-ev);
 #pragma unroll 1
           for (int r = ct >> 2; r < KT; r += 32) {
             // rows past the last: V has to be zeros (their weight is 0), K may be anything (their scores are masked)
             const bool zero = r - (ct >> 2) >= n;
-            Quarter k8, v8;
+            const Quarter kr = k8, vr = v8;
+            load_own(r + 32);
+            int ek = 0, ev = 0;      // a row with an infinity or NaN: K makes all its codes NaN
             if (!zero) {
-              load_own(r, k8, v8);
-              k8.split(k8.amax() < kInfBits ? ik : qnan(), r, ct & 3, sK + k0 * KSTAGE, sK + k1 * KSTAGE);
+              const uint32_t x = kr.amax(), y = vr.amax();
+              if (x < kInfBits) ek = bits_exp(x);
+              if (y < kInfBits) ev = bits_exp(y);
+              kr.split(x < kInfBits ? kv8::exp2i(-ek) : qnan(), r, ct & 3, sK + k0 * KSTAGE, sK + k1 * KSTAGE);
+            }
+            const float iv = kv8::exp2i(-ev);
+            if ((ct & 3) == 0) {
+              bar.own[g].k[r] = kv8::exp2i(ek);
+              bar.own[g].lv[r] = (float)ev;
+              bar.own[g].iv[r] = iv;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -801,7 +831,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
               uint4 x = make_uint4(0, 0, 0, 0);
               if (!zero) {
                 float f[8];
-                bf16x8_to_f32(v8.raw[i], f);
+                bf16x8_to_f32(vr.raw[i], f);
                 x = make_uint4(f16x2(f[0] * iv, f[1] * iv), f16x2(f[2] * iv, f[3] * iv), f16x2(f[4] * iv, f[5] * iv),
                                f16x2(f[6] * iv, f[7] * iv));
               }
@@ -863,46 +893,59 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           else
             wait_for(&bar.w_full[g], ph, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
           if (warp_live) {
-            const float4* run = pre ? bar.run[rs] : &bar.run_own[g];
-            const int rstep = pre ? 1 : 0;
             const bool partly = !__all_sync(0xffffffffu, lim >= KT);
             tc::fence_after_sync();
-            // 32 columns at a time, P into half the columns of the scores that it replaces
+            // 32 columns at a time, P into half the columns of the scores that it replaces. Own tiles, the rarer ones, have
+            // a copy of the loop of their own: with both forms in one the prefix tiles took 8 to 17 % longer
             float lt = 0.f;
+            auto weigh = [&](auto of_prefix) {
+              constexpr bool PRE = decltype(of_prefix)::value;
+              const float4* run = PRE ? bar.run[rs] : &bar.run_one;
+              const int rstep = PRE ? 1 : 0;
+              const float c1 = PRE ? rowc : 1.f;      // factor of the row's scores
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              float v[32];
-              load_scores(tSg + 32 * c, partly, lim - 32 * c, v);
-              uint32_t pk[16];
-              float lc;
+              for (int c = 0; c < 4; ++c) {
+                float v[32];
+                tmem_ld32(tSg + 32 * c, v);
+                if (!PRE) own_exponents(v, rowc, bar.own[g].k + 32 * c, bar.own[g].lv + 32 * c);
+                mask_scores(partly, lim - 32 * c, v);
+                uint32_t pk[16];
+                float lc;
 #pragma unroll 1
-              for (int tries = 0;; ++tries) {
-                const float sum = scores_exp(v, rowc, run + 2 * c * rstep, rstep, kOff - (mg == -INFINITY ? 0.f : mg), pk, lc);
-                const bool move = sum > kMost || mg == -INFINITY;
-                if (tries || !__any_sync(0xffffffffu, move)) break;
-                // the reference of the rows concerned moves to the largest score here, and what they have so far with it
-                const float m = scores_max(v, rowc, run + 2 * c * rstep, rstep);
-                float alpha = 1.f;
-                if (move && m > mg) {
-                  alpha = mg == -INFINITY ? 1.f : ex2(mg - m);
-                  mg = m;
+                for (int tries = 0;; ++tries) {
+                  const float shift = kOff - (mg == -INFINITY ? 0.f : mg);
+                  const float sum = PRE ? scores_exp(v, c1, run + 2 * c * rstep, rstep, shift, pk, lc)
+                                        : own_exp(v, bar.own[g].iv + 32 * c, shift, pk, lc);
+                  const bool move = sum > kMost || mg == -INFINITY;
+                  if (tries || !__any_sync(0xffffffffu, move)) break;
+                  // the reference of the rows concerned moves to the largest score here, and what they have so far with it
+                  const float m = scores_max(v, c1, run + 2 * c * rstep, rstep);
+                  float alpha = 1.f;
+                  if (move && m > mg) {
+                    alpha = mg == -INFINITY ? 1.f : ex2(mg - m);
+                    mg = m;
+                  }
+                  l *= alpha;
+                  lt *= alpha;
+                  if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                    tc::tmem_st_wait();
+                    scale_columns<true>(tSg, 2 * c, alpha);
+                    if (any) scale_columns<false>(tOg, 16, alpha);
+                  }
                 }
-                l *= alpha;
-                lt *= alpha;
-                if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                  tc::tmem_st_wait();
-                  scale_columns<true>(tSg, 2 * c, alpha);
-                  if (any) scale_columns<false>(tOg, 16, alpha);
-                }
+                lt += lc;
+                asm volatile(
+                    "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::
+                        "r"(tSg + 16 * c),
+                    "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7]), "r"(pk[8]),
+                    "r"(pk[9]), "r"(pk[10]), "r"(pk[11]), "r"(pk[12]), "r"(pk[13]), "r"(pk[14]), "r"(pk[15])
+                    : "memory");
               }
-              lt += lc;
-              asm volatile(
-                  "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::
-                      "r"(tSg + 16 * c),
-                  "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7]), "r"(pk[8]),
-                  "r"(pk[9]), "r"(pk[10]), "r"(pk[11]), "r"(pk[12]), "r"(pk[13]), "r"(pk[14]), "r"(pk[15])
-                  : "memory");
-            }
+            };
+            if (pre)
+              weigh(std::true_type{});
+            else
+              weigh(std::false_type{});
             l += lt;
             tc::tmem_st_wait();
             tc::fence_before_sync();
