@@ -1108,8 +1108,9 @@ __global__ void __launch_bounds__(KT) attn_kv8_merge_kernel(const __grid_constan
 // ------------------------------------------------------------------------------------------------ attention weight
 // mass[j] (+)= sum over the query rows R of 2^(S[R, j] c - lse2[R]). The product is transposed, S^T = K Q^T: keys are the
 // rows of the accumulator, so a thread owns a key and adds its row up in registers, with no sum across threads and no
-// atomics. The queries of a row tile share one power-of-two scale, so that the factor c = k_scale 2^k scale log2(e) is
-// the thread's own; lse2 comes from shared memory. Key tiles are dealt to the CTAs like the attention's; a CTA goes over
+// atomics. A query row's factor 2^k scale log2(e) (a power-of-two scale of its own, as in the attention that wrote its
+// lse) and its lse2 come from shared memory, the key's scale is the thread's own. A row that gives no weight (lse -inf) is
+// staged as zeros, whatever it holds. Key tiles are dealt to the CTAs like the attention's; a CTA goes over
 // its tiles of a (b, kv head) once per row tile of the queries (more than one: K comes from L2 after the first time).
 // Bound by the exponentials: 128 x 128 per key tile and row tile, 1024 clocks, against 512 of MMAs and 710 of HBM.
 // Roles: warp 0 TMA, warp 1 MMA, warps 4-15 three groups that take the key tiles in turn, each with an S buffer (a thread's
@@ -1125,9 +1126,8 @@ struct MassBars {
   uint32_t tmem_base;
   int abort_flag;
   int walk[7];
-  uint32_t red[2][4];
-  float factor[2];             // per staged row tile: 2^k scale log2(e)
-  alignas(16) float nlse[2][KT];   // -lse log2(e); -inf for rows that give no weight
+  alignas(16) float factor[2][KT];   // per staged query row: 2^k scale log2(e)
+  alignas(16) float nlse[2][KT];     // -lse log2(e); -inf for rows that give no weight
 };
 constexpr int MASS_SMEM = 1024 + 2 * 2 * KSTAGE /*Q*/ + MK * KSTAGE + (int)sizeof(MassBars);
 static_assert(MASS_SMEM <= 232448, "shared memory budget");
@@ -1247,41 +1247,41 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
   } else if (warp >= 4 + 4 * MS) {
     // ------------------------------------------------------------------ queries: four threads per row, 32 rows at a time
     const int ct = tid - 128 * (1 + MS);
-    const uint32_t cw = warp - 4 - 4 * MS;
     uint32_t seg = 0;
     for (; w.n > 0; w.next(p))
       for (int rt = 0; rt < q_rt; ++rt, ++seg) {
         const uint32_t qb = seg & 1;
-        uint32_t m = 0;
-#pragma unroll 1
-        for (int r = ct >> 2; r < KT; r += 32) {
-          const __nv_bfloat16* src = query_row(p, w.b, w.h, rt, r);
-          Quarter q;
+        Quarter q;
+        float nl;
+        // the next 32 rows are on their way while these are converted (the first ones ahead of the wait)
+        auto load = [&](int r) {
+          const __nv_bfloat16* src = r < KT ? query_row(p, w.b, w.h, rt, r) : nullptr;
+          nl = -INFINITY;
+          if (src) {
+            const int R = rt * KT + r, qi = p.by_G(R);
+            const float lse = a.lse_in[((int64_t)w.b * a.Lq + qi) * a.Hq + w.h * p.G + R - qi * p.G];
+            if (lse == -INFINITY)
+              src = nullptr;
+            else
+              nl = -lse * kLog2e;
+          }
           q.load(src ? src + 32 * (ct & 3) : nullptr);
-          const uint32_t x = q.amax();
-          m = max(m, x < kInfBits ? x : 0u);
-        }
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) bar.red[qb][cw] = m;
-        tc::named_bar_sync(kBarConv, 128);
-        const int k = bits_exp(max(max(bar.red[qb][0], bar.red[qb][1]), max(bar.red[qb][2], bar.red[qb][3])));
-        const float inv = kv8::exp2i(-k);
-        const int R = rt * KT + ct, qi = p.by_G(R);
-        float nl = -INFINITY;
-        if (R < p.n_rows) {
-          const float lse = a.lse_in[((int64_t)w.b * a.Lq + qi) * a.Hq + w.h * p.G + R - qi * p.G];
-          if (lse != -INFINITY) nl = -lse * kLog2e;
-        }
+        };
+        load(ct >> 2);
         if (seg >= 2) wait_for(&bar.q_empty[qb], ((seg >> 1) & 1) ^ 1, &bar.abort_flag, ST_TIMEOUT_PRODUCER);
-        bar.nlse[qb][ct] = nl;
-        if (ct == 0) bar.factor[qb] = kv8::exp2i(k) * (a.scale * kLog2e);
 #pragma unroll 1
         for (int r = ct >> 2; r < KT; r += 32) {
-          const __nv_bfloat16* src = query_row(p, w.b, w.h, rt, r);
-          Quarter q;
-          q.load(src ? src + 32 * (ct & 3) : nullptr);
-          // an infinity or NaN in a row makes its codes NaN, and with them its weight on every key
-          q.split(q.amax() < kInfBits ? inv : qnan(), r, ct & 3, sQ + qb * 2 * KSTAGE, sQ + (qb * 2 + 1) * KSTAGE);
+          const Quarter x = q;
+          const float n = nl;
+          load(r + 32);
+          const uint32_t m = x.amax();
+          const int k = m >= kInfBits ? 0 : bits_exp(m);
+          if ((ct & 3) == 0) {
+            // an infinity or NaN reaches the row's weight on every key
+            bar.factor[qb][r] = m >= kInfBits ? qnan() : kv8::exp2i(k) * (a.scale * kLog2e);
+            bar.nlse[qb][r] = n;
+          }
+          x.split(kv8::exp2i(-k), r, ct & 3, sQ + qb * 2 * KSTAGE, sQ + (qb * 2 + 1) * KSTAGE);
         }
         fence_async_smem();
         arrive(&bar.q_full[qb]);
@@ -1299,7 +1299,6 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
         const uint32_t qb = seg & 1;
         const int cols = min(KT, p.n_rows - rt * KT);
         wait_for(&bar.q_full[qb], (seg >> 1) & 1, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
-        const float f = bar.factor[qb];
         // another group may have added the last row tile to this group's tiles
         if (rt > 0) tc::named_bar_sync(kBarPair, 128 * MS);
         for (int t = w.ta; t < t_end; ++t, ++it) {
@@ -1316,20 +1315,20 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
             wait_for(&bar.s_full[sb], ph, &bar.abort_flag, ST_TIMEOUT_EPILOGUE);
             __syncwarp();
             tc::fence_after_sync();
-            const float c = f * ks;
-            const uint64_t c2 = pk2(c, c);
+            const uint64_t ks2 = pk2(ks, ks);
             uint64_t s2 = pk2(0.f, 0.f);
 #pragma unroll 1
             for (int j = 0; j < cols; j += 32) {
               float v[32];
               tmem_ld32(tS + sb * 128 + j + lane_off, v);
               const float4* nl = reinterpret_cast<const float4*>(bar.nlse[qb] + j);
+              const float4* fs = reinterpret_cast<const float4*>(bar.factor[qb] + j);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float4 n4 = nl[i];
+                const float4 n4 = nl[i], f4 = fs[i];
                 float x0, x1, x2, x3;
-                upk2(fma2(pk2(v[4 * i], v[4 * i + 1]), c2, pk2(n4.x, n4.y)), x0, x1);
-                upk2(fma2(pk2(v[4 * i + 2], v[4 * i + 3]), c2, pk2(n4.z, n4.w)), x2, x3);
+                upk2(fma2(pk2(v[4 * i], v[4 * i + 1]), mul2(ks2, pk2(f4.x, f4.y)), pk2(n4.x, n4.y)), x0, x1);
+                upk2(fma2(pk2(v[4 * i + 2], v[4 * i + 3]), mul2(ks2, pk2(f4.z, f4.w)), pk2(n4.z, n4.w)), x2, x3);
                 s2 = add2(s2, pk2(ex2(x0), ex2(x1)));
                 s2 = add2(s2, pk2(ex2(x2), ex2(x3)));
               }
