@@ -554,7 +554,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       uint32_t ks = 0, vs = 0;      // slots of the K and V rings so far
       uint32_t kq = 0, vq = 0;      // one past the last slot that this thread filled (for the drain)
       bool ok = true;
-      // 128 rows of codes: rows past the cache read as zeros, rows past the prefix are masked (K) or cleared (V)
+      // 128 rows of codes: rows past P read as zeros, rows past the prefix are masked (K) or cleared (V)
       auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full, int row, int bh) {
         tc::mbar_arrive_expect_tx(full, KSTAGE);
         asm volatile(
@@ -1356,13 +1356,16 @@ attn_mass_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
   }
 }
 
-int encode_codes(CUtensorMap* m, const void* codes, int64_t cap, int64_t bh) {
+// Map of bh heads of `rows` rows of codes, cap rows apart. Its extent is the rows that the call may read, not cap: a tile's
+// rows past them read as zeros and are never fetched (a cache may be a part of a longer one that ends with its last head's
+// rows).
+int encode_codes(CUtensorMap* m, const void* codes, int64_t rows, int64_t cap, int64_t bh) {
   EncodeTiledFn enc = encoder();
   if (!enc) {
     dllm_host::set_error("cuTensorMapEncodeTiled unavailable");
     return DLLM_ERR_CUDA;
   }
-  const cuuint64_t dims[3] = {128, (cuuint64_t)cap, (cuuint64_t)bh};
+  const cuuint64_t dims[3] = {128, (cuuint64_t)rows, (cuuint64_t)bh};
   const cuuint64_t str[2] = {128, (cuuint64_t)cap * 128};
   const cuuint32_t box[3] = {128, KT, 1}, es[3] = {1, 1, 1};
   const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, str, box, es,
@@ -1424,9 +1427,9 @@ int launch_attn_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
   p.n_cta = (int)std::min<int64_t>(num_sms(), most);
   CUtensorMap mk, mv;
   // without prefix rows no tile is loaded; the maps then describe the queries' memory, which exists
-  int st = a.P > 0 ? encode_codes(&mk, a.k_codes, a.cap, (int64_t)a.B * a.Hkv) : encode_codes(&mk, a.q, 1, 1);
+  int st = a.P > 0 ? encode_codes(&mk, a.k_codes, a.P, a.cap, (int64_t)a.B * a.Hkv) : encode_codes(&mk, a.q, 1, 1, 1);
   if (st) return st;
-  st = a.P > 0 ? encode_codes(&mv, a.v_codes, a.cap, (int64_t)a.B * a.Hkv) : encode_codes(&mv, a.q, 1, 1);
+  st = a.P > 0 ? encode_codes(&mv, a.v_codes, a.P, a.cap, (int64_t)a.B * a.Hkv) : encode_codes(&mv, a.q, 1, 1, 1);
   if (st) return st;
   st = set_max_smem<attn_kv8_tc_kernel>(SMEM);
   if (st) return st;
@@ -1448,7 +1451,7 @@ int launch_attn_mass_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
   const int64_t most = (int64_t)a.B * a.Hkv * ((a.P + KT - 1) / KT);
   p.n_cta = (int)std::min<int64_t>(num_sms(), most);
   CUtensorMap mk;
-  int st = encode_codes(&mk, a.k_codes, a.cap, (int64_t)a.B * a.Hkv);
+  int st = encode_codes(&mk, a.k_codes, a.P, a.cap, (int64_t)a.B * a.Hkv);
   if (st) return st;
   st = set_max_smem<attn_mass_kv8_tc_kernel>(MASS_SMEM);
   if (st) return st;

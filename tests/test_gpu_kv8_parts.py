@@ -1,0 +1,38 @@
+"""The 8-bit KV cache's calls on a part of a longer cache (GPU): rows [r0, cap) of every head, so that the last head's rows
+end where the memory ends. Each call gives the bits it gives on a copy of the part."""
+import pytest
+import torch
+
+from block_diffusion_moe_dllm_b200 import binding as bd
+from block_diffusion_moe_dllm_b200 import synth
+from test_gpu_kv8 import DEV, DT, cdiv, make_cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    bd.load()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("B,Hkv,cap,r0,S", [(1, 1, 200, 64, 32), (2, 3, 333, 48, 16), (1, 2, 129, 128, 128)])
+def test_attention_and_weights_of_a_part(dtype, d, B, Hkv, cap, r0, S):
+    Lq, Hq, P = 3, 2 * Hkv, cap - r0
+    kc, vc, ks, vs, _, _ = make_cache(B, Hkv, cap, d, S, 101)
+    q = synth.normal((B, Lq, Hq, d), 1.5, 101, "q", DEV, synth.torch_dtype(dtype))
+    got = []
+    for part in (True, False):
+        c = [x[:, :, r0:] if part else x[:, :, r0:].contiguous() for x in (kc, vc)]
+        s = [x[:, :, r0 // S:] if part else x[:, :, r0 // S:].contiguous() for x in (ks, vs)]
+        stride = cap if part else P
+        out = torch.full((B, Lq, Hq * d), float("nan"), dtype=q.dtype, device=DEV)
+        lse = torch.full((B, Lq, Hq), float("nan"), device=DEV)
+        # scales of a part are as far apart as the whole cache's: the copy's heads have fewer runs
+        bd.block_attn_kv8(q, *c, *s, out, B, Lq, Hq, Hkv, d, P, stride, S, 1, DT[dtype], lse=lse)
+        mass = torch.full((B, Hkv, stride), 3.0, device=DEV)
+        bd.attn_mass_kv8(q, c[0], s[0], lse, None, mass, B, Lq, Hq, Hkv, d, P, stride, S, DT[dtype])
+        assert torch.all(mass[:, :, P:] == 3.0)
+        got.append((out, lse, mass[:, :, :P]))
+        assert cdiv(stride, S) == (ks.shape[2] if part else cdiv(P, S))
+    assert all(torch.equal(x, y) for x, y in zip(*got)) and torch.isfinite(got[0][0]).all()
