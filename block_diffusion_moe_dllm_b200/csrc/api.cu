@@ -520,7 +520,7 @@ namespace {
 // Arrays of na and nb bytes share memory.
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return a && b && x < y + nb && y < x + na;
+  return a && b && na && nb && x < y + nb && y < x + na;
 }
 
 int check_kv8_format(const char* who, int d, int scale_len) {
@@ -548,10 +548,15 @@ bool outputs_apart(const void* const* p, const size_t* n, int count, int n_out) 
   return true;
 }
 
-// Bytes from the first to the last scale that a call on P rows of every (b, kv head) reads.
-size_t kv8_scales_read(size_t bh, int cap, int P, int scale_len) {
+// Bytes from the first to the last of the rows that a call uses: `rows` of each of `heads`, which lie cap rows apart (a cache
+// may be a part of a longer one).
+size_t kv8_span(size_t heads, int cap, int rows, size_t row_bytes) {
+  return rows > 0 ? ((heads - 1) * cap + rows) * row_bytes : 0;
+}
+// The same of scales, one per run of scale_len rows.
+size_t kv8_scale_span(size_t heads, int cap, int rows, int scale_len) {
   const size_t runs = ((size_t)cap + scale_len - 1) / scale_len;
-  return P ? ((bh - 1) * runs + ((size_t)P + scale_len - 1) / scale_len) * 4 : 0;
+  return rows > 0 ? ((heads - 1) * runs + ((size_t)rows + scale_len - 1) / scale_len) * 4 : 0;
 }
 
 // What the two attention calls check alike.
@@ -595,11 +600,15 @@ int dllm_kv8_store(const dllm_kv8_store_desc* d, const void* k, const void* v, c
   REQ(aligned16(k) && aligned16(v) && aligned16(k_codes) && aligned16(v_codes), DLLM_ERR_ALIGN,
       "kv8_store: k, v and the code tensors must be 16-byte aligned");
   {
-    const size_t bh = (size_t)d->B * d->Hkv, src = bh * d->cap_src * d->d * esize(d->dtype), cb = bh * d->cap * d->d,
-                 sb = bh * ((d->cap + d->scale_len - 1) / d->scale_len) * 4;
-    const void* const p[] = {k_codes, v_codes, k_scale, v_scale, k, v, dst_rows};      // k and v may be the same
-    const size_t n[] = {cb, cb, sb, sb, src, src, (size_t)d->B * 4};
-    REQ(outputs_apart(p, n, 7, 4), DLLM_ERR_INVALID_ARG, "kv8_store: an output overlaps another array");
+    // rows named by device values can be any
+    const size_t bh = (size_t)d->B * d->Hkv;
+    const int to = dst_rows ? d->cap : d->dst_row + d->n, from = src_pos ? d->cap_src : d->src_row + d->n;
+    const size_t src = kv8_span(bh, d->cap_src, from, d->d * esize(d->dtype)), cb = kv8_span(bh, d->cap, to, d->d),
+                 sb = kv8_scale_span(bh, d->cap, to, d->scale_len);
+    const size_t pb = d->n ? ((size_t)(d->B - 1) * d->pos_stride + d->n) * 4 : 0;
+    const void* const p[] = {k_codes, v_codes, k_scale, v_scale, k, v, dst_rows, src_pos};      // k and v may be the same
+    const size_t n[] = {cb, cb, sb, sb, src, src, (size_t)d->B * 4, pb};
+    REQ(outputs_apart(p, n, 8, 4), DLLM_ERR_INVALID_ARG, "kv8_store: an output overlaps another array");
   }
   if (d->n == 0) return DLLM_OK;
   Kv8StoreArgs a;
@@ -637,15 +646,15 @@ int dllm_block_attn_kv8(const dllm_attn_kv8_desc* d, const void* q, const void* 
       DLLM_ERR_ALIGN, "block_attn_kv8: q, out, codes and own rows must be 16-byte aligned");
   {
     const size_t rows = (size_t)d->B * d->Lq * d->Hq, bh = (size_t)d->B * d->Hkv, qb = rows * d->d * esize(d->dtype);
-    // from the first to the last row that is read: a cache may be a part of a longer one
-    const size_t cb = d->P ? ((bh - 1) * d->cap + d->P) * d->d : 0, sb = kv8_scales_read(bh, d->cap, d->P, d->scale_len),
-                 ob = ((bh - 1) * d->cap_own + d->Lq) * d->d * esize(d->dtype);
-    const void* const p[] = {out, lse, q, k_codes, v_codes, k_scale, v_scale, k_own, v_own, prefix_len};
-    const size_t n[] = {qb, rows * 4, qb, cb, cb, sb, sb, ob, ob, (size_t)d->B * 4};
-    REQ(outputs_apart(p, n, 10, 2), DLLM_ERR_INVALID_ARG, "block_attn_kv8: an output overlaps another array");
+    const size_t cb = kv8_span(bh, d->cap, d->P, d->d), sb = kv8_scale_span(bh, d->cap, d->P, d->scale_len),
+                 ob = kv8_span(bh, d->cap_own, d->Lq, d->d * esize(d->dtype)), wb = dllm_block_attn_kv8_workspace_size(d);
+    const void* const p[] = {ws, out, lse, q, k_codes, v_codes, k_scale, v_scale, k_own, v_own, prefix_len};
+    const size_t n[] = {wb, qb, rows * 4, qb, cb, cb, sb, sb, ob, ob, (size_t)d->B * 4};
+    REQ(outputs_apart(p + 1, n + 1, 10, 2), DLLM_ERR_INVALID_ARG, "block_attn_kv8: an output overlaps another array");
+    st = check_ws(ws, ws_bytes, wb);
+    if (st) return st;
+    REQ(outputs_apart(p, n, 11, 1), DLLM_ERR_INVALID_ARG, "block_attn_kv8: the workspace overlaps another array");
   }
-  st = check_ws(ws, ws_bytes, dllm_block_attn_kv8_workspace_size(d));
-  if (st) return st;
   Carver c(ws);
   Kv8AttnArgs a = {};
   a.B = d->B; a.Lq = d->Lq; a.Hq = d->Hq; a.Hkv = d->Hkv; a.d = d->d; a.blk_len = d->blk_len; a.P = d->P;
@@ -668,15 +677,17 @@ int dllm_attn_mass_kv8(const dllm_attn_mass_desc* d, const void* q, const void* 
   REQ(d->P == 0 || (k_codes && k_scale), DLLM_ERR_INVALID_ARG, "attn_mass_kv8: NULL cache");
   REQ(aligned16(q) && aligned16(k_codes), DLLM_ERR_ALIGN, "attn_mass_kv8: q and codes must be 16-byte aligned");
   {
-    const size_t rows = (size_t)d->B * d->Lq * d->Hq, bh = (size_t)d->B * d->Hkv, mb = bh * d->cap * 4;
-    const size_t cb = d->P ? ((bh - 1) * d->cap + d->P) * d->d : 0, sb = kv8_scales_read(bh, d->cap, d->P, d->scale_len);
-    const void* const p[] = {mass_out, mass_in == mass_out ? nullptr : mass_in, q, k_codes, k_scale, lse, prefix_len};
-    const size_t n[] = {mb, mb, rows * d->d * esize(d->dtype), cb, sb, rows * 4, (size_t)d->B * 4};
-    REQ(outputs_apart(p, n, 7, 1), DLLM_ERR_INVALID_ARG,
+    const size_t rows = (size_t)d->B * d->Lq * d->Hq, bh = (size_t)d->B * d->Hkv, mb = kv8_span(bh, d->cap, d->P, 4);
+    const size_t cb = kv8_span(bh, d->cap, d->P, d->d), sb = kv8_scale_span(bh, d->cap, d->P, d->scale_len),
+                 wb = dllm_attn_mass_kv8_workspace_size(d);
+    const void* const p[] = {ws, mass_out, mass_in == mass_out ? nullptr : mass_in, q, k_codes, k_scale, lse, prefix_len};
+    const size_t n[] = {wb, mb, mb, rows * d->d * esize(d->dtype), cb, sb, rows * 4, (size_t)d->B * 4};
+    REQ(outputs_apart(p + 1, n + 1, 7, 1), DLLM_ERR_INVALID_ARG,
         "attn_mass_kv8: mass_out overlaps another array (mass_in may be the same one)");
+    st = check_ws(ws, ws_bytes, wb);
+    if (st) return st;
+    REQ(outputs_apart(p, n, 8, 1), DLLM_ERR_INVALID_ARG, "attn_mass_kv8: the workspace overlaps another array");
   }
-  st = check_ws(ws, ws_bytes, dllm_attn_mass_kv8_workspace_size(d));
-  if (st) return st;
   if (d->P == 0) return DLLM_OK;
   Kv8AttnArgs a = {};
   a.B = d->B; a.Lq = d->Lq; a.Hq = d->Hq; a.Hkv = d->Hkv; a.d = d->d; a.blk_len = 1; a.P = d->P; a.cap = d->cap;
@@ -710,19 +721,20 @@ int dllm_kv8_evict(const dllm_kv8_evict_desc* d, const void* k_codes, const void
   REQ(aligned16(k_codes) && aligned16(v_codes) && aligned16(k_out) && aligned16(v_out), DLLM_ERR_ALIGN,
       "kv8_evict: code tensors must be 16-byte aligned");
   {
-    const size_t bh = (size_t)d->B * d->Hkv, cb = bh * d->cap * d->d, co = bh * d->cap_out * d->d;
-    const size_t sb = bh * ((d->cap + d->scale_len - 1) / d->scale_len) * 4,
-                 so = bh * ((d->cap_out + d->scale_len - 1) / d->scale_len) * 4;
-    const size_t hs = (size_t)d->B * (d->per_head ? d->Hkv : 1);
-    const void* const p[] = {k_out,   v_out,   k_scale_out, v_scale_out, mass_out, keep_pos, len_out,
-                             k_codes, v_codes, k_scale,     v_scale,     mass,     pos,      prefix_len};
-    const size_t nb = (size_t)d->B * 4;
-    const size_t n[] = {co, co, so, so, bh * d->cap_out * 4, hs * d->cap_out * 4, nb,
-                        cb, cb, sb, sb, bh * d->cap * 4,     hs * d->cap * 4,     nb};
-    REQ(outputs_apart(p, n, 14, 7), DLLM_ERR_INVALID_ARG, "kv8_evict: an output overlaps another array");
+    const size_t bh = (size_t)d->B * d->Hkv, hs = (size_t)d->B * (d->per_head ? d->Hkv : 1);
+    const int P = d->P, kept = std::min(d->n_keep, P);      // rows read and written of every head, at most
+    const size_t cb = kv8_span(bh, d->cap, P, d->d), co = kv8_span(bh, d->cap_out, kept, d->d),
+                 sb = kv8_scale_span(bh, d->cap, P, d->scale_len), so = kv8_scale_span(bh, d->cap_out, kept, d->scale_len),
+                 nb = (size_t)d->B * 4, wb = dllm_kv8_evict_workspace_size(d);
+    const void* const p[] = {ws,      k_out,   v_out,   k_scale_out, v_scale_out, mass_out, keep_pos,  len_out,
+                             k_codes, v_codes, k_scale, v_scale,     mass,        pos,      prefix_len};
+    const size_t n[] = {wb, co, co, so, so, kv8_span(bh, d->cap_out, kept, 4), kv8_span(hs, d->cap_out, kept, 4), nb,
+                        cb, cb, sb, sb, kv8_span(bh, d->cap, P, 4),            kv8_span(hs, d->cap, P, 4),        nb};
+    REQ(outputs_apart(p + 1, n + 1, 14, 7), DLLM_ERR_INVALID_ARG, "kv8_evict: an output overlaps another array");
+    st = check_ws(ws, ws_bytes, wb);
+    if (st) return st;
+    REQ(outputs_apart(p, n, 15, 1), DLLM_ERR_INVALID_ARG, "kv8_evict: the workspace overlaps another array");
   }
-  st = check_ws(ws, ws_bytes, dllm_kv8_evict_workspace_size(d));
-  if (st) return st;
   Carver c(ws);
   Kv8EvictArgs a;
   a.B = d->B; a.Hkv = d->Hkv; a.d = d->d; a.P = d->P; a.cap = d->cap; a.n_keep = d->n_keep; a.cap_out = d->cap_out;
