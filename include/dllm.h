@@ -482,9 +482,19 @@ DLLM_API int dllm_kv8_store(const dllm_kv8_store_desc* desc, const void* k, cons
  *   k_own, v_own [B, Hkv, cap_own, d] in the storage type, rows [0, Lq) (both NULL: the prefix only)
  *   out          [B, Lq, Hq * d], 16-byte aligned; zeros where a query sees no key
  *   lse          [B, Lq, Hq] fp32 (nullable): log of the sum of exp(score) over the query's keys, -inf without keys
- * out and lse overlap no other array. scale <= 0 selects 1/sqrt(d). Any Hq a multiple of Hkv. bf16: d == 128. Own V rows must be finite (a query's weight
- * on a row it does not see is 0, and 0 times infinity is not). bf16 reads V scales below 2^-64 as 2^-64 and holds the
- * weights in f16 (11 bits; those below 2^-27 of the row's largest so far count as 0), their sums in fp32.
+ * out, lse and the workspace overlap no other array. scale <= 0 selects 1/sqrt(d). Any Hq a multiple of Hkv.
+ * Own V rows must be finite: a query's weight on a row it does not see is 0, and 0 times infinity is not.
+ *
+ * bf16 (d == 128) runs on the tensor cores:
+ *   queries, own K  two E4M3 parts with a power-of-two scale of each row: exact to 2^-17.8 of the row's largest magnitude
+ *   own V           f16 with a power-of-two scale of each row; V scales of the cache below 2^-64 are read as 2^-64
+ *   weights         f16, and what is rounded is weight times V scale, relative to a reference that is at most the row's
+ *                   largest such product: 11 bits down to 2^-16 of it, fewer below, 0 below 2^-27. n keys lose at most
+ *                   n * 2^-26 times the largest product times their codes, in every column, whichever row is the large
+ *                   one. Keys whose product is below 2^-126 of the largest leave the weights' sum (and lse) too: V scales of
+ *                   one row's keys should lie within 2^100 of one another.
+ *   sums, lse       fp32
+ * fp32 computes all of it in fp32.
  */
 typedef struct {
   int32_t B, Lq, Hq, Hkv, d;
@@ -509,6 +519,7 @@ DLLM_API size_t dllm_block_attn_kv8_workspace_size(const dllm_attn_kv8_desc* des
  * order: the same inputs give the same bits.
  *   mass_in (nullable: zeros), mass_out [B, Hkv, cap] fp32, the same array or disjoint ones, and no other array's memory;
  *   rows past a prefix are left as they were.
+ * bf16 holds queries as dllm_block_attn_kv8 does, each row with a scale of its own. Rows of lse -inf may hold anything.
  */
 typedef struct {
   int32_t B, Lq, Hq, Hkv, d;

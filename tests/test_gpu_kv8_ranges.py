@@ -1,5 +1,5 @@
 """The 8-bit KV cache's attention against the fp64 formulas where values of very different sizes meet (GPU): own rows
-that a query does not see, and own rows of different sizes.
+that a query does not see, own rows of different sizes, and one key above all others.
 
 Bounds, per element (u16 = 2^-8 and u32 = 2^-24: half a step of bf16 and fp32). With p_j the softmax weights, s_j the
 scores, m the largest of them, a_j the largest magnitude of V row j and n the visible keys:
@@ -22,8 +22,9 @@ import torch
 
 from block_diffusion_moe_dllm_b200 import binding as bd
 from block_diffusion_moe_dllm_b200 import synth
+from oracle import kv8_oracle as K8
 from _util import to64
-from test_gpu_kv8 import DEV, make_cache
+from test_gpu_kv8 import DEV, codes64, make_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +127,54 @@ def test_own_rows_of_different_sizes(dtype, d, P, Lq, blk):
     vo = (own_rows((1, Hkv, Lq, d), 82, "vo", torch.float32) * torch.exp2(ev)[:, None]).to(t)
     out, lse = attend(q, kc, vc, ks, vs, ko, vo, P, 16, blk)
     check(out, lse, to64(q), kv[:, :, :P], vv[:, :, :P], to64(ko), to64(vo), blk)
+
+
+# ------------------------------------------------------------------------------------------------ one key above all
+@pytest.mark.parametrize("dtype,d,P", [("bf16", 128, 9000), ("f32", 64, 3000), ("bf16", 128, 33000)])
+@pytest.mark.parametrize("gap", [4.0, 9.0, 13.0, 17.0])
+def test_one_key_above_all_others(dtype, d, P, gap):
+    """The first key's score lies `gap` above the rest of a long prefix, so that the others are together as heavy as it is,
+    or each far below what f16 resolves beside it."""
+    t = synth.torch_dtype(dtype)
+    S, Hkv, Hq, Lq = 32, 1, 2, 2
+    kc, vc, ks, vs, kv, vv = make_cache(1, Hkv, P, d, S, 83)
+    q = own_rows((1, Lq, Hq, d), 83, "q", torch.float32) * 0.25
+    # the first key is all +-64 * scale, with the queries' signs in a common half of the columns
+    sign = torch.where(torch.arange(d, device=DEV) % 3 == 0, -1.0, 1.0)
+    kc[0, 0, 0] = torch.where(sign > 0, 0x68, 0xE8).to(torch.uint8)         # +-64
+    k0 = 64.0 * float(ks[0, 0, 0])
+    q = (q + sign * gap * np.sqrt(d) / (d * k0)).to(t)
+    kv = K8.values(codes64(kc), to64(ks), S)
+    out, lse = attend(q, kc, vc, ks, vs, None, None, P, S, 1)
+    check(out, lse, to64(q), kv, vv, None, None, 1)
+
+
+def test_one_v_run_above_all_others():
+    """A V run whose scale is 2^16 times the others' and whose codes fill one column: the other columns lose what the bound
+    allows, n * 2^-25 of the largest weight times V, and no more; the log-sum-exp loses nothing."""
+    B, Lq, Hq, Hkv, d, P, S = 1, 4, 4, 2, 128, 320, 32
+    kc, vc, ks, vs, _, _ = make_cache(B, Hkv, P, d, S, 84)
+    vc[:, :, 64:96] = 0
+    vc[:, :, 64:96, 17] = 0x7E                                              # 448
+    vs[:, :, 2] *= 2.0 ** 16
+    kv, vv = K8.values(codes64(kc), to64(ks), S), K8.values(codes64(vc), to64(vs), S)
+    q = own_rows((B, Lq, Hq, d), 84, "q", torch.bfloat16)
+    out, lse = attend(q, kc, vc, ks, vs, None, None, P, S, 1)
+    check(out, lse, to64(q), kv, vv, None, None, 1)
+
+
+# ------------------------------------------------------------------------------------------------ no keys at all
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 3e38])
+def test_queries_without_keys_are_zero_whatever_they_hold(dtype, d, bad):
+    t = synth.torch_dtype(dtype)
+    B, Lq, Hq, Hkv, P, S = 3, 5, 4, 2, 200, 32
+    kc, vc, ks, vs, kv, vv = make_cache(B, Hkv, P, d, S, 85)
+    q = own_rows((B, Lq, Hq, d), 85, "q", t)
+    q[1, 2:, 1, 7] = bad
+    q[1, 3] = bad
+    lens = torch.tensor([P, 0, 131], dtype=torch.int32, device=DEV)
+    out, lse = attend(q, kc, vc, ks, vs, None, None, P, S, 1, lens=lens)
+    assert not out[1].any() and torch.all(lse[1] == -float("inf"))
+    for b, n in ((0, P), (2, 131)):
+        check(out[b: b + 1], lse[b: b + 1], to64(q[b: b + 1]), kv[b: b + 1, :, :n], vv[b: b + 1, :, :n], None, None, 1)
