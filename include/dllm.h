@@ -459,7 +459,13 @@ DLLM_API int dllm_denoise_step_views(const dllm_model* model, const dllm_state* 
  *             list as dllm_prefix_retain writes it); positions outside [0, cap_src) are stored as zeros
  *   dst_rows  [B] int32 (nullable): first cache row written of each batch row, dst_row for all without it. It starts a
  *             run (a multiple of scale_len) and leaves room for n rows; a batch row whose device value does not is
- *             left as it was. The last run may end early: its other rows keep their codes.
+ *             left as it was, and NOT reported: the call returns DLLM_OK and that row's K/V are not stored.
+ *             The last run may end early: its other rows keep their codes.
+ * So rows are appended a run at a time: a batch row can only go on where its length is a multiple of scale_len. What
+ * follows a partial run stays with the caller, in the storage type, until it fills one, or the run is stored again from
+ * its first row. A caller that takes lengths from the device (dllm_kv8_evict's len_out is prefix_len where that is below
+ * n_keep) makes sure of that before. Rows of different lengths are stored in one call by a src_pos that is -1 past each
+ * row's own end: those tokens are zeros and do not enter a run's scale.
  */
 typedef struct {
   int32_t B, Hkv, d, n;

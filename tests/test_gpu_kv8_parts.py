@@ -36,3 +36,38 @@ def test_attention_and_weights_of_a_part(dtype, d, B, Hkv, cap, r0, S):
         got.append((out, lse, mass[:, :, :P]))
         assert cdiv(stride, S) == (ks.shape[2] if part else cdiv(P, S))
     assert all(torch.equal(x, y) for x, y in zip(*got)) and torch.isfinite(got[0][0]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ragged_rows_stored_in_one_call(dtype):
+    """Rows of lengths of their own by a position list that is -1 past each end: what lies there leaves no trace, each row
+    is stored as it is alone, and the next block goes behind a row whose length is a multiple of the run."""
+    B, Hkv, d, n, S, cap = 3, 2, 64, 200, 32, 256
+    lens = (77, 200, 96)
+    t = synth.torch_dtype(dtype)
+    k, v = (synth.normal((B, Hkv, n, d), 1.0, 102, x, DEV, t) for x in ("k", "v"))
+    for b, m in enumerate(lens):
+        k[b, :, m:], v[b, :, m:] = 1e30, float("nan")
+    pos = torch.arange(n, dtype=torch.int32, device=DEV).repeat(B, 1)
+    pos = torch.where(pos < torch.tensor(lens, device=DEV)[:, None], pos, -1)
+
+    def empty(rows):
+        return ([torch.zeros((rows, Hkv, cap, d), dtype=torch.uint8, device=DEV) for _ in range(2)],
+                [torch.zeros((rows, Hkv, cap // S), device=DEV) for _ in range(2)])
+
+    codes, scale = empty(B)
+    bd.kv8_store(k, v, *codes, *scale, B, Hkv, d, n, n, cap, S, DT[dtype], src_pos=pos)
+    for b, m in enumerate(lens):
+        c1, s1 = empty(1)
+        bd.kv8_store(k[b: b + 1], v[b: b + 1], *c1, *s1, 1, Hkv, d, m, n, cap, S, DT[dtype])
+        for x, y in zip(codes + scale, c1 + s1):
+            rows = m if x.dtype == torch.uint8 else cdiv(m, S)
+            assert torch.equal(x[b, :, :rows], y[0, :, :rows])
+            assert x.dtype != torch.uint8 or not x[b, :, m:n].any()
+    # of the three lengths only 96 starts a run: the others are left as they were
+    before = [x.clone() for x in codes + scale]
+    blk = [synth.normal((B, Hkv, 32, d), 1.0, 103, x, DEV, t) for x in ("k", "v")]
+    bd.kv8_store(*blk, *codes, *scale, B, Hkv, d, 32, 32, cap, S, DT[dtype],
+                 dst_rows=torch.tensor(lens, dtype=torch.int32, device=DEV))
+    for x, y in zip(codes + scale, before):
+        assert torch.equal(x[:2], y[:2]) and not torch.equal(x[2], y[2])
