@@ -1,5 +1,5 @@
-"""The 8-bit KV cache's calls on a part of a longer cache (GPU): rows [r0, cap) of every head, so that the last head's rows
-end where the memory ends. Each call gives the bits it gives on a copy of the part."""
+"""The 8-bit KV cache's calls on parts of longer arrays and on rows of lengths of their own (GPU). Each gives the bits it
+gives on a copy of the part, or on the row alone."""
 import pytest
 import torch
 
@@ -18,6 +18,7 @@ def _lib():
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
 @pytest.mark.parametrize("B,Hkv,cap,r0,S", [(1, 1, 200, 64, 32), (2, 3, 333, 48, 16), (1, 2, 129, 128, 128)])
 def test_attention_and_weights_of_a_part(dtype, d, B, Hkv, cap, r0, S):
+    """Rows [r0, cap) of every head: the last head's rows end where the memory ends."""
     Lq, Hq, P = 3, 2 * Hkv, cap - r0
     kc, vc, ks, vs, _, _ = make_cache(B, Hkv, cap, d, S, 101)
     q = synth.normal((B, Lq, Hq, d), 1.5, 101, "q", DEV, synth.torch_dtype(dtype))
@@ -28,13 +29,11 @@ def test_attention_and_weights_of_a_part(dtype, d, B, Hkv, cap, r0, S):
         stride = cap if part else P
         out = torch.full((B, Lq, Hq * d), float("nan"), dtype=q.dtype, device=DEV)
         lse = torch.full((B, Lq, Hq), float("nan"), device=DEV)
-        # scales of a part are as far apart as the whole cache's: the copy's heads have fewer runs
         bd.block_attn_kv8(q, *c, *s, out, B, Lq, Hq, Hkv, d, P, stride, S, 1, DT[dtype], lse=lse)
         mass = torch.full((B, Hkv, stride), 3.0, device=DEV)
         bd.attn_mass_kv8(q, c[0], s[0], lse, None, mass, B, Lq, Hq, Hkv, d, P, stride, S, DT[dtype])
         assert torch.all(mass[:, :, P:] == 3.0)
         got.append((out, lse, mass[:, :, :P]))
-        assert cdiv(stride, S) == (ks.shape[2] if part else cdiv(P, S))
     assert all(torch.equal(x, y) for x, y in zip(*got)) and torch.isfinite(got[0][0]).all()
 
 
@@ -71,3 +70,24 @@ def test_ragged_rows_stored_in_one_call(dtype):
                  dst_rows=torch.tensor(lens, dtype=torch.int32, device=DEV))
     for x, y in zip(codes + scale, before):
         assert torch.equal(x[:2], y[:2]) and not torch.equal(x[2], y[2])
+
+
+def test_fewer_tiles_than_ctas():
+    """Device lengths far below P: most CTAs of the launch have no share of the tiles, with several heads to a row. The
+    results are those of a call whose P says so: the same bits for the weights, and for the outputs one rounding (bf16's
+    step is at most 2^-7 of the value) of sums that were split elsewhere."""
+    B, Lq, Hq, Hkv, d, P, S = 3, 5, 8, 4, 128, 8192, 64
+    lens = torch.tensor([1, 0, 130], dtype=torch.int32, device=DEV)
+    kc, vc, ks, vs, _, _ = make_cache(B, Hkv, P, d, S, 104)
+    q = synth.normal((B, Lq, Hq, d), 1.5, 104, "q", DEV, torch.bfloat16)
+    want = None
+    for most in (130, P):
+        out = torch.full((B, Lq, Hq * d), float("nan"), dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((B, Lq, Hq), float("nan"), device=DEV)
+        mass = torch.full((B, Hkv, P), 2.0, device=DEV)
+        bd.block_attn_kv8(q, kc, vc, ks, vs, out, B, Lq, Hq, Hkv, d, most, P, S, 1, bd.BF16, prefix_len=lens, lse=lse)
+        bd.attn_mass_kv8(q, kc, ks, lse, None, mass, B, Lq, Hq, Hkv, d, most, P, S, bd.BF16, prefix_len=lens)
+        want = want or (out, lse, mass)
+    assert torch.equal(mass, want[2]) and torch.equal(lse[1], want[1][1])
+    assert torch.allclose(out.float(), want[0].float(), rtol=2 ** -7, atol=1e-5) and not out[1].any()
+    assert torch.allclose(lse[::2], want[1][::2], rtol=1e-6, atol=1e-6)
