@@ -289,15 +289,25 @@ def unmask(logits, row_pos, n_rows_dev, tokens, mask, sel, nsel, conf, remaining
                                  stream_handle(stream)))
 
 
-def _device_stream(t, stream):
-    """The stream's handle, after checking that the call's tensors are on the current device (the library launches
-    there)."""
+def _raw_stream(current):
+    """The handle of the current stream of the current device."""
     import torch
-    dev, current = t.get_device(), torch.cuda.current_device()
-    if dev != current:
-        raise DllmError(ERR_INVALID_ARG, f"tensors on device {dev}, current device {current}")
-    # the handle alone: building the Stream object of the current stream takes 3 us of a 10 us call
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(current)
+    # the handle alone, where this torch has a way to it: building the Stream object takes 3 us of a 10 us call
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(current) if raw else stream_handle()
+
+
+def _launch_args(stream, *tensors):
+    """Addresses of a call's tensors (None stays None) and, last, its stream's handle. All tensors have to be on the current
+    device: the library launches there, and an address of the host or of another device would fault it."""
+    import torch
+    current = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != current:
+            raise DllmError(ERR_INVALID_ARG, f"tensor on {t.device}, current device {current}")
+    at = [None if t is None else t.data_ptr() for t in tensors]
+    at.append(stream.cuda_stream if stream is not None else _raw_stream(current))
+    return at
 
 
 def _stream_workspace(ws, need, device, stream):
@@ -316,8 +326,8 @@ def kv8_store(k, v, k_codes, v_codes, k_scale, v_scale, B, Hkv, d, n, cap_src, c
     lib = load()
     desc = Kv8StoreDesc(B, Hkv, d, n, cap_src, src_row, cap, dst_row, scale_len, dtype,
                         n if pos_stride is None else pos_stride)
-    return check(lib.dllm_kv8_store(C.byref(desc), ptr(k), ptr(v), ptr(src_pos), ptr(dst_rows), ptr(k_codes),
-                                    ptr(v_codes), ptr(k_scale), ptr(v_scale), _device_stream(k_codes, stream)))
+    return check(lib.dllm_kv8_store(C.byref(desc), *_launch_args(stream, k, v, src_pos, dst_rows, k_codes, v_codes, k_scale,
+                                                                 v_scale)))
 
 
 def block_attn_kv8(q, k_codes, v_codes, k_scale, v_scale, out, B, Lq, Hq, Hkv, d, P, cap, scale_len, blk_len, dtype,
@@ -327,9 +337,8 @@ def block_attn_kv8(q, k_codes, v_codes, k_scale, v_scale, out, B, Lq, Hq, Hkv, d
     desc = AttnKv8Desc(B, Lq, Hq, Hkv, d, blk_len, P, cap, cap_own, scale_len, dtype, scale)
     need = lib.dllm_block_attn_kv8_workspace_size(C.byref(desc))
     ws = _stream_workspace(ws, need, q.device, stream)
-    return check(lib.dllm_block_attn_kv8(C.byref(desc), ptr(q), ptr(k_codes), ptr(v_codes), ptr(k_scale),
-                                         ptr(v_scale), ptr(prefix_len), ptr(k_own), ptr(v_own), ptr(out), ptr(lse),
-                                         ws.addr, ws.nbytes, _device_stream(q, stream)))
+    *at, _, st = _launch_args(stream, q, k_codes, v_codes, k_scale, v_scale, prefix_len, k_own, v_own, out, lse, ws.buf)
+    return check(lib.dllm_block_attn_kv8(C.byref(desc), *at, ws.addr, ws.nbytes, st))
 
 
 def attn_mass_kv8(q, k_codes, k_scale, lse, mass_in, mass_out, B, Lq, Hq, Hkv, d, P, cap, scale_len, dtype,
@@ -339,8 +348,8 @@ def attn_mass_kv8(q, k_codes, k_scale, lse, mass_in, mass_out, B, Lq, Hq, Hkv, d
     desc = AttnMassDesc(B, Lq, Hq, Hkv, d, P, cap, scale_len, dtype, scale, decay)
     need = lib.dllm_attn_mass_kv8_workspace_size(C.byref(desc))
     ws = _stream_workspace(ws, need, q.device, stream)
-    return check(lib.dllm_attn_mass_kv8(C.byref(desc), ptr(q), ptr(k_codes), ptr(k_scale), ptr(prefix_len), ptr(lse),
-                                        ptr(mass_in), ptr(mass_out), ws.addr, ws.nbytes, _device_stream(q, stream)))
+    *at, _, st = _launch_args(stream, q, k_codes, k_scale, prefix_len, lse, mass_in, mass_out, ws.buf)
+    return check(lib.dllm_attn_mass_kv8(C.byref(desc), *at, ws.addr, ws.nbytes, st))
 
 
 def kv8_evict(k_codes, v_codes, k_scale, v_scale, mass, k_out, v_out, k_scale_out, v_scale_out, mass_out, keep_pos,
@@ -351,10 +360,9 @@ def kv8_evict(k_codes, v_codes, k_scale, v_scale, mass, k_out, v_out, k_scale_ou
     desc = Kv8EvictDesc(B, Hkv, d, P, cap, n_keep, cap_out, scale_len, n_first, n_last, per_head)
     need = lib.dllm_kv8_evict_workspace_size(C.byref(desc))
     ws = _stream_workspace(ws, need, mass.device, stream)
-    return check(lib.dllm_kv8_evict(C.byref(desc), ptr(k_codes), ptr(v_codes), ptr(k_scale), ptr(v_scale), ptr(mass),
-                                    ptr(prefix_len), ptr(pos), ptr(k_out), ptr(v_out), ptr(k_scale_out),
-                                    ptr(v_scale_out), ptr(mass_out), ptr(keep_pos), ptr(len_out), ws.addr, ws.nbytes,
-                                    _device_stream(mass, stream)))
+    *at, _, st = _launch_args(stream, k_codes, v_codes, k_scale, v_scale, mass, prefix_len, pos, k_out, v_out, k_scale_out,
+                              v_scale_out, mass_out, keep_pos, len_out, ws.buf)
+    return check(lib.dllm_kv8_evict(C.byref(desc), *at, ws.addr, ws.nbytes, st))
 
 
 def status_check(ws, stream=None):

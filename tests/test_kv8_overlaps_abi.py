@@ -1,4 +1,4 @@
-"""The 8-bit KV cache entry points without a GPU: which arrays may lie beside or between others, and which not."""
+"""The 8-bit KV cache entry points without a GPU: which arrays may lie beside or between others, and where tensors may be."""
 import ctypes as C
 
 import pytest
@@ -95,3 +95,57 @@ def test_parts_of_longer_arrays_may_lie_side_by_side(lib):
     for off, code_ in ((mass, bd.ERR_WORKSPACE), (mass - 4, bd.ERR_INVALID_ARG)):
         assert lib.dllm_attn_mass_kv8(C.byref(a), 1 * GB, 2 * GB, 3 * GB, None, 4 * GB, 5 * GB + off, 5 * GB + r0 * 4, None,
                                       1 << 40, None) == code_
+
+
+# ------------------------------------------------------------------------------------------------ the binding
+class On:
+    """A tensor's place, as the binding looks at it."""
+
+    def __init__(self, device, nbytes=1 << 20):
+        self.device, self.nbytes, self.addr, self.buf = device, nbytes, 256, self
+
+    def get_device(self):
+        return self.device
+
+    def data_ptr(self):
+        return 256
+
+
+@pytest.mark.parametrize("where", [-1, 1])
+def test_each_tensor_has_to_be_on_the_current_device(monkeypatch, where):
+    """Every tensor of every call, one at a time on the host (-1) or on another device, is refused before the library is
+    called."""
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    sizes = dict(B=1, Hkv=1, d=128, cap=16, scale_len=16)
+    q = dict(Lq=1, Hq=1, P=16, dtype=bd.BF16)
+    calls = [(bd.kv8_store, ["k", "v", "k_codes", "v_codes", "k_scale", "v_scale", "src_pos", "dst_rows"],
+              dict(sizes, n=16, cap_src=16, dtype=bd.BF16)),
+             (bd.block_attn_kv8, ["q", "k_codes", "v_codes", "k_scale", "v_scale", "out", "prefix_len", "k_own", "v_own", "lse",
+                                  "ws"], dict(sizes, **q, blk_len=1, cap_own=1)),
+             (bd.attn_mass_kv8, ["q", "k_codes", "k_scale", "lse", "mass_in", "mass_out", "prefix_len", "ws"],
+              dict(sizes, **q)),
+             (bd.kv8_evict, ["k_codes", "v_codes", "k_scale", "v_scale", "mass", "k_out", "v_out", "k_scale_out",
+                             "v_scale_out", "mass_out", "keep_pos", "len_out", "prefix_len", "pos", "ws"],
+              dict(sizes, P=16, n_keep=8, cap_out=8))]
+    for call, names, rest in calls:
+        for bad in names:
+            tensors = {n: On(where if n == bad else 0, 1 << 30) for n in names}
+            with pytest.raises(bd.DllmError) as e:
+                call(**tensors, **rest)
+            assert e.value.code == bd.ERR_INVALID_ARG and "current device" in str(e.value), (call.__name__, bad)
+
+
+def test_stream_handle_without_the_short_way(monkeypatch):
+    import torch
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert bd._raw_stream(0) == 77
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 1000 + dev, raising=False)
+    assert bd._raw_stream(3) == 1003
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    assert bd._launch_args(Stream, None, On(0)) == [None, 256, 77] and bd._launch_args(None) == [1000]
