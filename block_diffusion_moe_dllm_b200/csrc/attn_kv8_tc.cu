@@ -235,7 +235,7 @@ DLLM_DEV void make_walk(const Params& p, int* walk) {
   for (int o = 16; o > 0; o >>= 1) T += __shfl_xor_sync(0xffffffffu, T, o);
   const Share share(T, p.n_cta);
   const uint32_t x = share.first(blockIdx.x), n = share.first(blockIdx.x + 1) - x;
-  uint32_t before = 0, rem = 0, in_row = 0;      // stays 0 in a CTA without a share
+  uint32_t before = 0, rem = 0, in_row = (uint32_t)a.Hkv;      // of a CTA without a share: any but 0 tiles a head
   int b = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const uint32_t own = b0 == 0 ? mine : (b0 + lane < a.B ? row_tiles(p, b0 + lane) : 0);
@@ -256,18 +256,15 @@ DLLM_DEV void make_walk(const Params& p, int* walk) {
     before += __shfl_sync(0xffffffffu, v, 31);
   }
   if (lane == 0) {
-    int h = 0, rt = 0, len = 0;
-    if (in_row) {
-      const uint32_t per_h = in_row / (uint32_t)a.Hkv;
-      h = (int)(rem / per_h);
-      rem -= (uint32_t)h * per_h;
-      len = kv8::prefix_len(a.lens, b, a.P);
-      const int tp = cdiv128(len);
-      for (; rt + 1 < p.n_rt; ++rt) {
-        const uint32_t t = (uint32_t)(max(1, tp + cdiv128(own_keys(p, rt))) + p.extra);
-        if (rem < t) break;
-        rem -= t;
-      }
+    const uint32_t per_h = in_row / (uint32_t)a.Hkv;
+    const int h = (int)(rem / per_h);
+    rem -= (uint32_t)h * per_h;
+    const int len = kv8::prefix_len(a.lens, b, a.P), tp = cdiv128(len);
+    int rt = 0;
+    for (; rt + 1 < p.n_rt; ++rt) {
+      const uint32_t t = (uint32_t)(max(1, tp + cdiv128(own_keys(p, rt))) + p.extra);
+      if (rem < t) break;
+      rem -= t;
     }
     walk[0] = b; walk[1] = h; walk[2] = rt; walk[3] = (int)rem; walk[4] = (int)n; walk[5] = len; walk[6] = (int)T;
   }
