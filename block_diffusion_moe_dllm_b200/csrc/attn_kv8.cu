@@ -36,25 +36,16 @@ SimtPlan simt_plan(int B, int Lq, int Hq, int Hkv, int P, int own) {
   return p;
 }
 
-DLLM_DEV void load4(const float* p, float* f) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-}
-
 // ROWS rows of the queries, scaled, into shared memory (pitch d + 4); rows past the last are zero.
 DLLM_DEV void load_rows(const Kv8AttnArgs& a, int b, int h, int R0, float mul, float* qs) {
-  constexpr int VE = 4;
-  const int G = a.Hq / a.Hkv, vpr = a.d / VE, pitch = a.d + 4;
+  const int G = a.Hq / a.Hkv, vpr = a.d / 4, pitch = a.d + 4;
   for (int i = threadIdx.x; i < ROWS * vpr; i += 256) {
-    const int r = i / vpr, c = (i - r * vpr) * VE, R = R0 + r;
-    float f[VE];
-#pragma unroll
-    for (int k = 0; k < VE; ++k) f[k] = 0.f;
+    const int r = i / vpr, c = (i - r * vpr) * 4, R = R0 + r;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (R < a.Lq * G)
-      load4(static_cast<const float*>(a.q) + (((int64_t)b * a.Lq + R / G) * a.Hq + h * G + R % G) * a.d + c, f);
-#pragma unroll
-    for (int k = 0; k < VE; k += 4)
-      *reinterpret_cast<float4*>(qs + r * pitch + c + k) = make_float4(f[k] * mul, f[k + 1] * mul, f[k + 2] * mul, f[k + 3] * mul);
+      x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
+                                           (((int64_t)b * a.Lq + R / G) * a.Hq + h * G + R % G) * a.d + c);
+    *reinterpret_cast<float4*>(qs + r * pitch + c) = make_float4(x.x * mul, x.y * mul, x.z * mul, x.w * mul);
   }
 }
 
@@ -80,17 +71,12 @@ DLLM_DEV void load_codes(const uint8_t* codes, const float* scale, int64_t bh, i
 }
 
 DLLM_DEV void load_own(const float* src, int64_t bh, int cap_own, int d, int j0, int nk, float* dst) {
-  constexpr int VE = 4;
-  const int vpr = d / VE, pitch = d + 4;
+  const int vpr = d / 4, pitch = d + 4;
   for (int i = threadIdx.x; i < KB * vpr; i += 256) {
-    const int r = i / vpr, c = (i - r * vpr) * VE;
-    float f[VE];
-#pragma unroll
-    for (int k = 0; k < VE; ++k) f[k] = 0.f;
-    if (r < nk) load4(src + (bh * cap_own + j0 + r) * (int64_t)d + c, f);
-#pragma unroll
-    for (int k = 0; k < VE; k += 4)
-      *reinterpret_cast<float4*>(dst + r * pitch + c + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+    const int r = i / vpr, c = (i - r * vpr) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < nk) x = *reinterpret_cast<const float4*>(src + (bh * cap_own + j0 + r) * (int64_t)d + c);
+    *reinterpret_cast<float4*>(dst + r * pitch + c) = x;
   }
 }
 
@@ -227,8 +213,8 @@ __global__ void __launch_bounds__(256, 1) attn_kv8_simt_kernel(const Kv8AttnArgs
       float* dst = static_cast<float*>(a.out) + qh * d;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        if (c0 < d) dst[c0 + c] = (o[r][c] * inv);
-        if (c1 < d) dst[c1 + c] = (o[r][4 + c] * inv);
+        if (c0 < d) dst[c0 + c] = o[r][c] * inv;
+        if (c1 < d) dst[c1 + c] = o[r][4 + c] * inv;
       }
       if (cg == 0 && a.lse_out) a.lse_out[qh] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
     }
@@ -262,7 +248,7 @@ __global__ void __launch_bounds__(256) attn_kv8_simt_merge_kernel(const Kv8AttnA
   const int64_t qh = ((int64_t)b * a.Lq + R / G) * a.Hq + h * G + R % G;
 #pragma unroll
   for (int c = 0; c < 4; ++c)
-    if (lane + 32 * c < d) static_cast<float*>(a.out)[qh * d + lane + 32 * c] = (o[c] * inv);
+    if (lane + 32 * c < d) static_cast<float*>(a.out)[qh * d + lane + 32 * c] = o[c] * inv;
   if (lane == 0 && a.lse_out) a.lse_out[qh] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 

@@ -107,17 +107,6 @@ DLLM_DEV bool ready(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// n / d for 0 <= n < 2^31 (n * m >> shift; see attn_tc.cu).
-struct FastDiv {
-  uint32_t m, shift;
-  DLLM_DEV int operator()(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> shift); }
-};
-FastDiv fast_div(int d) {
-  uint32_t sh = 0;
-  while ((1u << sh) < (uint32_t)d) ++sh;
-  return {(uint32_t)((((uint64_t)1 << (31 + sh)) + (uint64_t)d - 1) / (uint64_t)d), 31 + sh};
-}
-
 // Per key of an own tile: K scale, log2(V scale), 1 / V scale (read as pairs).
 struct OwnScales {
   alignas(16) float k[KT], lv[KT], iv[KT];

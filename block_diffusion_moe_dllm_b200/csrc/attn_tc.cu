@@ -66,21 +66,13 @@ static_assert(sizeof(Bars) <= BARS_BYTES, "barrier block exceeds its shared-memo
 struct AttnTcParams {
   int B, Lq, Hq, Hkv, G, QT, n_qtiles, n_keys, cap, blk_len, q_pos0;
   int n_splits, tiles_per_split;
-  uint32_t blk_magic, blk_shift;   // key position / blk_len = (pos * blk_magic) >> blk_shift for 0 <= pos < 2^31
+  FastDiv by_blk;             // key position / blk_len
   float scale_log2;
   const int32_t* key_pos;
   __nv_bfloat16* out;   // [B, Lq, Hq, 128]
   int32_t* status;
   const int32_t* live;  // nullable: *live == 0 = a denoising pass with no masked position left (nothing to do)
 };
-
-// Integer division by the block length without the divide sequence (which would queue on the special-function unit
-// behind the softmax's exponentials): multiply by m = ceil(2^(31+s) / d), 2^(s-1) < d <= 2^s, and keep the bits
-// above 31 + s; exact for 0 <= n < 2^31 since n (m d - 2^(31+s)) < 2^(31+s) (Granlund and Montgomery, "Division by
-// invariant integers using multiplication", 1994).
-__device__ __forceinline__ int div_blk(int n, uint32_t m, uint32_t shift) {
-  return (int)(((uint64_t)(uint32_t)n * m) >> shift);
-}
 
 // Named barrier over n threads that also ORs a predicate across them: every participant gets the same answer.
 __device__ __forceinline__ bool bar_sync_or(int id, int n, bool pred) {
@@ -296,7 +288,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int key = jt * KT + gtid;
         int rel = kNoKey;
         if (key < n_keys_eff) {
-          const int kb = div_blk(p.key_pos ? p.key_pos[(int64_t)b * p.n_keys + key] : key, p.blk_magic, p.blk_shift);
+          const int kb = p.by_blk(p.key_pos ? p.key_pos[(int64_t)b * p.n_keys + key] : key);
           rel = max(-32768, min(32766, kb - qblk_min));   // the queries' relative blocks lie in [0, 128]
         }
         bar.kblk[grp][i & 1][gtid] = (short)rel;
@@ -592,12 +584,7 @@ int launch_attn_tc(const AttnArgs& a, int32_t* status, cudaStream_t s) {
   AttnTcParams p;
   p.B = a.B; p.Lq = a.Lq; p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv; p.n_keys = a.n_keys; p.cap = a.cap;
   p.blk_len = a.blk_len; p.q_pos0 = a.q_pos0;
-  {
-    uint32_t sh = 0;
-    while ((1u << sh) < (uint32_t)a.blk_len) ++sh;                     // 2^(sh-1) < blk_len <= 2^sh
-    p.blk_magic = (uint32_t)((((uint64_t)1 << (31 + sh)) + (uint64_t)a.blk_len - 1) / (uint64_t)a.blk_len);
-    p.blk_shift = 31 + sh;
-  }
+  p.by_blk = fast_div(a.blk_len);
   plan_tc(a.B, a.Lq, a.Hq, a.Hkv, a.n_keys, p.QT, p.n_qtiles, p.n_splits, p.tiles_per_split);
   const float scale = a.scale > 0.f ? a.scale : 1.0f / sqrtf((float)a.d);
   p.scale_log2 = scale * 1.4426950408889634f;

@@ -1,5 +1,5 @@
 // Device and host helpers of the tensor-core attention kernels: bounded waits, TMEM row loads, packed fp32 arithmetic,
-// the descriptor of an MN-major operand, and the driver's tensor-map encoder.
+// division by a constant of the launch, the descriptor of an MN-major operand, and the driver's tensor-map encoder.
 #pragma once
 #include "common.cuh"
 #include "tc.cuh"
@@ -20,6 +20,19 @@ __device__ __forceinline__ uint64_t sdesc_mn128(uint32_t addr, uint32_t lbo) {
   d |= (uint64_t)1u << 46;
   d |= (uint64_t)2u << 61;
   return d;
+}
+
+// n / d for 0 <= n < 2^31 without the divide sequence (which would queue on the special-function unit behind the softmax's
+// exponentials): multiply by m = ceil(2^(31+s) / d), 2^(s-1) < d <= 2^s, and keep the bits above 31 + s; exact since
+// n (m d - 2^(31+s)) < 2^(31+s) (Granlund and Montgomery, "Division by invariant integers using multiplication", 1994).
+struct FastDiv {
+  uint32_t m, shift;
+  __device__ __forceinline__ int operator()(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> shift); }
+};
+inline FastDiv fast_div(int d) {
+  uint32_t s = 0;
+  while ((1u << s) < (uint32_t)d) ++s;
+  return {(uint32_t)((((uint64_t)1 << (31 + s)) + (uint64_t)d - 1) / (uint64_t)d), 31 + s};
 }
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
