@@ -177,12 +177,17 @@ __global__ void __launch_bounds__(256, 1) attn_kv8_simt_kernel(const Kv8AttnArgs
       ps[(4 * rg + r) * PD + cg + 16] = p1;
     }
     __syncwarp();                 // a row's weights are written and read by the same half-warp
+    // own keys that a row does not see are left out: their V may be infinite or NaN
+    int seen[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) seen[r] = pre ? nk : lim[r] - j0;
     for (int j = 0; j < nk; ++j) {
       float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
       if (c0 < d) v0 = *reinterpret_cast<const float4*>(vs + j * pitch + c0);
       if (c1 < d) v1 = *reinterpret_cast<const float4*>(vs + j * pitch + c1);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
+        if (j >= seen[r]) continue;
         const float w = ps[(4 * rg + r) * PD + j];
         o[r][0] = fmaf(w, v0.x, o[r][0]);
         o[r][1] = fmaf(w, v0.y, o[r][1]);

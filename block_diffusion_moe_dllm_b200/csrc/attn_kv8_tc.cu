@@ -801,24 +801,28 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             const bool zero = r - (ct >> 2) >= n;
             const Quarter kr = k8, vr = v8;
             load_own(r + 32);
-            int ek = 0, ev = 0;      // a row with an infinity or NaN: K makes all its codes NaN
+            // A row with an infinity or NaN: K makes all its codes NaN; V is zeros (0 times anything else is not 0 for the
+            // queries that do not see it) and its exponent NaN, which reaches the queries that do
+            int ek = 0, ev = 0;
+            bool bad = false;
             if (!zero) {
               const uint32_t x = kr.amax(), y = vr.amax();
               if (x < kInfBits) ek = bits_exp(x);
-              if (y < kInfBits) ev = bits_exp(y);
+              bad = y >= kInfBits;
+              if (!bad) ev = bits_exp(y);
               kr.split(x < kInfBits ? kv8::exp2i(-ek) : qnan(), r, ct & 3, sK + k0 * KSTAGE, sK + k1 * KSTAGE);
             }
             const float iv = kv8::exp2i(-ev);
             if ((ct & 3) == 0) {
               bar.own[g].k[r] = kv8::exp2i(ek);
-              bar.own[g].lv[r] = (float)ev;
+              bar.own[g].lv[r] = bad ? qnan() : (float)ev;
               bar.own[g].iv[r] = iv;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int gr = 4 * (ct & 3) + i;      // granule of 8 values: chunk gr >> 3
               uint4 x = make_uint4(0, 0, 0, 0);
-              if (!zero) {
+              if (!zero && !bad) {
                 float f[8];
                 bf16x8_to_f32(vr.raw[i], f);
                 x = make_uint4(f16x2(f[0] * iv, f[1] * iv), f16x2(f[2] * iv, f[3] * iv), f16x2(f[4] * iv, f[5] * iv),

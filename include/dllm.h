@@ -489,7 +489,8 @@ DLLM_API int dllm_kv8_store(const dllm_kv8_store_desc* desc, const void* k, cons
  *   out          [B, Lq, Hq * d], 16-byte aligned; zeros where a query sees no key
  *   lse          [B, Lq, Hq] fp32 (nullable): log of the sum of exp(score) over the query's keys, -inf without keys
  * out, lse and the workspace overlap no other array. scale <= 0 selects 1/sqrt(d). Any Hq a multiple of Hkv.
- * Own V rows must be finite: a query's weight on a row it does not see is 0, and 0 times infinity is not.
+ * Own rows that a query does not see may hold anything. An infinity or NaN in an own V row that it sees makes its output NaN
+ * in every column (bf16), or infinite or NaN in the columns concerned (fp32).
  *
  * bf16 (d == 128) runs on the tensor cores:
  *   queries, own K  two E4M3 parts with a power-of-two scale of each row: exact to 2^-17.8 of the row's largest magnitude

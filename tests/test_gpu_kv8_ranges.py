@@ -107,6 +107,25 @@ def test_own_rows_out_of_sight_change_nothing(dtype, d, P, Lq, blk, seen, size):
 
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("P,Lq,blk,seen", [(0, 70, 1, 40), (140, 70, 1, 5), (33, 200, 1, 131), (16, 200, 4, 20)])
+@pytest.mark.parametrize("holds", [float("nan"), float("inf"), -float("inf")])
+def test_own_rows_out_of_sight_may_hold_anything(dtype, d, P, Lq, blk, seen, holds):
+    """A padded chunk: rows from `seen` on are infinite or NaN as a whole or in one element. The queries before give the bits
+    that they give beside ordinary rows; those that see such a V row give NaN."""
+    t = synth.torch_dtype(dtype)
+    Hq = Hkv = 2
+    kc, vc, ks, vs, _, _ = make_cache(1, Hkv, max(P, 1), d, 16, 86)
+    q, ko, vo = (own_rows(s, 86, x, t) for x, s in (("q", (1, Lq, Hq, d)), ("ko", (1, Hkv, Lq, d)), ("vo", (1, Hkv, Lq, d))))
+    out, lse = attend(q, kc, vc, ks, vs, ko, vo, P, 16, blk)
+    k2, v2 = ko.clone(), vo.clone()
+    v2[:, 0, seen:], k2[:, 0, seen:] = holds, holds
+    v2[:, 1, seen, 9] = holds
+    out2, lse2 = attend(q, kc, vc, ks, vs, k2, v2, P, 16, blk)
+    assert torch.equal(out[:, :seen], out2[:, :seen]) and torch.equal(lse[:, :seen], lse2[:, :seen])
+    assert torch.isnan(out2[:, seen:, 0]).all() and not torch.isfinite(out2[:, seen:, 1, 9]).any()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
 @pytest.mark.parametrize("P,Lq,blk", [(0, 32, 32), (100, 130, 1)])
 def test_own_rows_of_different_sizes(dtype, d, P, Lq, blk):
     """Own values from 2^-12 to 2^4, ordinary own keys beside small ones and beside keys 2^14 times as large (in one column
