@@ -4,8 +4,8 @@
 // Work: the (query, head of the group) rows of a (batch row, kv head) are cut into tiles of 128 rows, each a unit of
 // ceil(len[b] / 128) prefix key tiles and the own key tiles its last query sees. All units' key tiles in a row are
 // dealt to one CTA per SM in equal contiguous shares, a unit's end counting for some tiles too, so rows of different
-// lengths, few rows and many rows all keep every SM busy equally long; a unit that spans several CTAs leaves its partial results (unnormalised o, m, l
-// per row) in the workspace and a second kernel joins them.
+// lengths, few rows and many rows all keep every SM busy equally long; a unit that spans several CTAs leaves its partial
+// results (unnormalised o, m, l per row) in the workspace and a second kernel joins them.
 //
 // Per key tile of 128:
 //   S = Q K^T   kind::f8f6f4, K's codes straight from the cache by TMA (never converted). The queries are exact
@@ -14,14 +14,16 @@
 //               same fp32 S. fp8 MMAs run at twice the bf16 rate, so the two cost what one bf16 product would.
 //               Own keys are split the same way by the converter warps (two parts: four products), each with a
 //               power-of-two scale of its own, and own V rows too: no row's precision depends on another row, least of all
-//               on one that the query does not see.
+//               on one that the query does not see (a scale for 128 own keys was 5 % faster in the smallest calls, and let
+//               hidden rows change the results of earlier queries).
 //   softmax     one thread per row; x = S * (2^k scale log2(e) k_scale) + log2(v_scale) - m: the V scale of each run rides
 //               in the exponent, so that P V needs no scaled copy of V; the row sum divides it out again run by run.
 //               P = 2^(x + 2) as f16. The reference m is not a running maximum: it is the largest of the first 32 scores
 //               that a row sees, and moves (rescaling O and the P of the tile so far) only when 32 weights add up to more
 //               than 30000, that is before one could leave f16's range. So the scores are read once, and no maximum is
-//               taken on the way. A weight keeps 11 bits down to 2^-16 of the reference and is dropped below 2^-27 (n
-//               keys lose at most n 2^-27 of the largest weight).
+//               taken on the way. What is rounded is weight times V scale: it keeps 11 bits down to 2^-16 of the
+//               reference and is dropped below 2^-27 (n keys lose at most n 2^-26 of the largest such product times their
+//               codes, where the reference has moved and rounded them twice).
 //   O += P V    kind::f16 with A = P from TMEM and B = V as f16 (every E4M3 value is one), written from the codes by four
 //               converter warps into the MN-major layout.
 // Tensor time of a tile: 8 + 8 MMAs of 64 clocks, and about 250 clocks for each of the two changes of the instruction
@@ -31,10 +33,10 @@
 // of its own in TMEM and references of its own; their results are joined at the end of a unit. Measured on the way, 8 x 32
 // queries of 16 heads over 32768 keys: two threads per row on the same tile 134 us; one O with a reference that the groups
 // pass on to each other and a pass for the maximum 105 us.
-// Measured (with the joining kernel): those 8 rows 92-103 us (2.6-2.9 TB/s of codes, 0.4 of the bf16 tensor rate), 16 x 32
-// queries over up to 2688 keys 30 us, one row over 1024 keys 14.5 us. Bound by a group's chain (its S waits for the P V
-// before it: about 2100 clocks a tile with two groups in flight), in small calls by set-up (2 us to the first load, 5 to
-// the first score) and the joining kernel.
+// Measured (with the joining kernel, 1965 MHz but for the long case's power limit): those 8 rows 103-108 us (2.5-2.6 TB/s of
+// codes, 0.4 of the bf16 tensor rate), 16 x 32 queries over up to 2688 keys 31.6 us, one row over 1024 keys 15.8 us. Bound
+// by a group's chain (its S waits for the P V before it: about 2100 clocks a tile with two groups in flight), in small
+// calls by set-up (2 us to the first load, 5 to the first score) and the joining kernel.
 //
 // Roles: warp 0 TMA, warp 1 MMA, warps 2 and 3 the runs' scales (alternate prefix tiles), warps 4-7 and 8-11 softmax (even
 // and odd tiles), warps 12-15 convert Q, V and the own rows. Warps whose rows are all past the last only
@@ -57,8 +59,9 @@ constexpr int VTILE = 2 * 128 * 64 * 2;    // V of a tile as f16: two 64-wide ch
 constexpr int VCHUNK = VTILE / 2;
 constexpr int NK = 3, NV = 2, NB = 2;      // stages of the K and V code rings; f16 V buffers
 // Key tiles that a unit's end (products, merge of the halves, output, the next unit's start) counts for in the CTAs' shares.
-// Measured with 0 / 3 / 4 / 5 / 8 (us): 16 x 2688 33.0 / 30.2 / 30.0 / 30.9 / 31.9, 8 x 32768 95.7 / 92.0 / 91.6 / 91.7 /
-// 92.6, 64 x 4001 single tokens 83.0 / 73.9 / 71.7 / 71.7 / 74.8, 2 x 500 rows on 4000 keys 83.6 / 81.6 / 83.7 / 81.2 / 84.0.
+// Measured with 0 / 3 / 4 / 5 / 8 (us, the middle of three runs in turn; runs of one differ by 0.5 at most): 16 x 2688 34.6 /
+// 31.7 / 31.6 / 32.6 / 33.9, 8 x 32768 110.1 / 108.2 / 107.3 / 107.3 / 107.2, 64 x 4001 single tokens 86.3 / 76.5 / 73.1 / 72.9 /
+// 76.1, 2 x 500 rows on 4000 keys 78.2 / 77.4 / 77.7 / 76.7 / 80.7: 4 and 5 are alike, 3 and 8 lose somewhere.
 constexpr int kUnitEnd = 4;
 constexpr float kMost = 30000.f;           // 32 weights that add up to more move the reference
 constexpr float kOff = 2.f;                // P is 2^2 times the weight relative to the reference
@@ -1105,10 +1108,13 @@ __global__ void __launch_bounds__(KT) attn_kv8_merge_kernel(const __grid_constan
 // lse) and its lse2 come from shared memory, the key's scale is the thread's own. A row that gives no weight (lse -inf) is
 // staged as zeros, whatever it holds. Key tiles are dealt to the CTAs like the attention's; a CTA goes over
 // its tiles of a (b, kv head) once per row tile of the queries (more than one: K comes from L2 after the first time).
-// Bound by the exponentials: 128 x 128 per key tile and row tile, 1024 clocks, against 512 of MMAs and 710 of HBM.
+// Bound by the exponentials: 128 x 128 per key tile and row tile, 1024 clocks, against 512 of MMAs and 710 of HBM; 16 x 32
+// queries over up to 2688 keys 16.6 us, 4 x 32 over 32768 34 us (31.9 with one query scale for a row tile, a packed product
+// less per two weights, which cost small rows beside large ones their precision).
 // Roles: warp 0 TMA, warp 1 MMA, warps 4-15 three groups that take the key tiles in turn, each with an S buffer (a thread's
-// loads, exponentials and sums follow one another, so two groups left the special-function units half idle: 4 rows of
-// 32768 keys, 128 rows a kv head, 35.3 us with two, 31.0 with three, 30.5 with four), warps 16-19 stage the queries.
+// loads, exponentials and sums follow one another, so two groups leave the special-function units half idle: 4 rows of
+// 32768 keys, 128 rows a kv head, 36.6 us with two, 34.3 with three, 35.5 with four, which spill; 16 x 2688 17.2, 16.6 and
+// 19.0), warps 16-19 stage the queries.
 constexpr int MK = 5, MS = 3;              // stages of the K ring, S buffers = groups
 constexpr int MASS_NT = 128 * (2 + MS);
 struct MassBars {
@@ -1411,7 +1417,7 @@ int launch_attn_kv8_tc(const Kv8AttnArgs& a, cudaStream_t s) {
   p.merge_shift = 3;
   while (p.merge_shift < 7 && (1 << p.merge_shift) < p.n_rows) ++p.merge_shift;
   // most tiles there can be (lengths may be shorter): no more CTAs than those. With a CTA for every tile the ends are not
-  // counted: the extra tiles would only bring CTAs without work (block of 1 x 1024: 14.3 us without them, 14.5 with)
+  // counted: the extra tiles would only bring CTAs without work (block of 1 x 1024: 15.8 us either way)
   const int64_t tp = (a.P + KT - 1) / KT;
   int64_t most = (int64_t)a.B * a.Hkv * (p.n_rt * (a.k_own ? tp : std::max<int64_t>(tp, 1)) + p.own_sum);
   p.extra = most > num_sms() ? kUnitEnd : 0;
